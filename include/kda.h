@@ -631,6 +631,128 @@ KDA_API int kda_graph_launch(kda_graph *g, void *stream);
 /* Release a graph (NULL is a no-op). Do not destroy a graph whose replay may still run. */
 KDA_API int kda_graph_destroy(kda_graph *g);
 
+/* ---------------------------------------------------------------------------------
+ * Paged key-value cache and its attention: the softmax-attention layers that a hybrid stack puts
+ * between its KDA layers (Glm5NextLayer: a layer's mixer is the KDA block or attention over a
+ * `PagedKvCache` with block tables). K and V rows live in fixed pages; a sequence is a slot of the
+ * page table. One table serves every layer: a page index names that page of all layers' pools.
+ *
+ * Everything below is device memory of the caller; the struct itself is passed by host pointer.
+ * Invariants (the calls here keep them; a caller that writes the arrays itself keeps them too):
+ * entries of a slot's table row at or past ceil(seq_len / page_size) are -1, ref[p] is the number of
+ * table entries that name page p, and a page that several slots share is full in each of them but
+ * where kda_kv_truncate has cut into it. Calls that change one cache must be ordered (one stream, or
+ * events). No call needs the lengths on the host, and every call may be captured into a CUDA graph.
+ */
+typedef struct kda_kv_cache {
+    kda_bf16 *k, *v;        /* layer 0's pools: [num_pages, kv_heads, page_size, head_dim] BF16 each     */
+    int *page_table;        /* [max_seqs, max_pages] page indices, -1 for none                           */
+    int *seq_len;           /* [max_seqs] cached tokens per slot                                         */
+    int *ref;               /* [num_pages] table entries per page; 0 = free                              */
+    int *scratch;           /* kda_kv_scratch_bytes() bytes for the bookkeeping calls; contents on entry
+                               do not matter                                                             */
+    long long layer_stride; /* elements from one layer's pool to the next (same for k and v)             */
+    int layers;
+    int num_pages;
+    int page_size;          /* 16, 32, 64, 128 or 256 tokens                                             */
+    int kv_heads;
+    int head_dim;           /* 64 or 128                                                                 */
+    int max_seqs, max_pages;
+} kda_kv_cache;
+
+/* Bytes of kda_kv_cache.scratch for a cache of these sizes (0 if one is not positive). */
+KDA_API size_t kda_kv_scratch_bytes(int num_pages, int max_seqs);
+
+/* kda_kv_reserve — room for add[i] more tokens in slot slots[i], i < n: the pages that the longer
+ * sequence needs are taken from the free ones (ref 0), the lowest index first, in list order, and
+ * seq_len grows by add[i]. The rows themselves are then written layer by layer with kda_kv_append.
+ * Where the slot's last page is partly filled and shared (after kda_kv_truncate), the slot first gets
+ * a copy of its own (copy-on-write; its filled rows are copied in all layers).
+ *   slots  DEVICE int32 [n], or NULL: slot i;  add  DEVICE int32 [n], >= 0;  n <= max_seqs
+ * A slot that is out of range, listed before, or asked to pass max_pages latches KDA_ERR_INVALID_ARG and
+ * stays as it is. When the pages run out, the slots that no longer fit (those whose pages, counted
+ * in list order over all slots, pass the number of free ones) stay as they are and
+ * KDA_ERR_CAPACITY is latched. */
+KDA_API int kda_kv_reserve(const kda_kv_cache *cache, const int *slots, const int *add, int n, void *stream);
+
+/* kda_kv_fork — slot child[i] becomes a copy of slot parent[i], i < n (parallel samples, beams): the
+ * full pages are shared (ref + 1); a partly filled last page gets a page of its own, the lowest free
+ * one in list order, into which its filled rows are copied in all layers.
+ *   parent, child  DEVICE int32 [n], n <= max_seqs; a parent may be listed any number of times
+ * Every parent is taken as it stands at the call's start. A pair with a slot out of range, with
+ * parent = child, with a child listed before or a child that is not empty (seq_len 0) latches
+ * KDA_ERR_INVALID_ARG and is skipped; out of pages as kda_kv_reserve. */
+KDA_API int kda_kv_fork(const kda_kv_cache *cache, const int *parent, const int *child, int n, void *stream);
+
+/* kda_kv_truncate — slot slots[i] keeps its first new_len[i] tokens (0 frees the slot; a verify's
+ * rejected draft rows are cut off the same way): the pages past them leave its table row, their
+ * ref drops by one, and a page whose ref reaches 0 is free.
+ *   slots  DEVICE int32 [n] or NULL (slot i);  new_len  DEVICE int32 [n], 0 <= new_len[i] <= seq_len;  n <= max_seqs
+ * A slot out of range, listed before or with another new_len latches KDA_ERR_INVALID_ARG and stays. */
+KDA_API int kda_kv_truncate(const kda_kv_cache *cache, const int *slots, const int *new_len, int n, void *stream);
+
+/* kda_kv_compact — moves the live pages (ref > 0) to the front of the pools: with L live pages, the
+ * i-th live page at or past index L goes to the i-th free index below L, in all layers; the
+ * table and ref follow. Pages below L stay where they are.
+ *   live  DEVICE int32 [1] that receives L, or NULL */
+KDA_API int kda_kv_compact(const kda_kv_cache *cache, int *live, void *stream);
+
+/* kda_kv_append — packed new K and V rows of one layer into their sequences' pages: the n_i rows of
+ * sequence i (rows [cu_seqlens[i], cu_seqlens[i+1])) are its last n_i tokens, i.e. row t goes to
+ * position seq_len - n_i + t of slot slots[i] (kda_kv_reserve has counted them already).
+ *   k_new, v_new  [total_tokens, kv_heads * head_dim] BF16, row stride ld elements (a multiple of 8, so
+ *                 the k and v columns of packed q|k|v projection rows can be passed as they are)
+ *   cu_seqlens    DEVICE int32 [B + 1];  slots  DEVICE int32 [B] or NULL (slot i)
+ * Rows at or past cu_seqlens[B] are not read. A sequence with bad bounds, a slot out of range or listed
+ * before, more rows than tokens, or a row whose table entry is no page or a page that several slots
+ * share is skipped and latches KDA_ERR_INVALID_ARG. */
+KDA_API int kda_kv_append(const kda_kv_cache *cache, int layer, const kda_bf16 *k_new, const kda_bf16 *v_new,
+                          long long ld, const int *cu_seqlens, const int *slots, int B, int total_tokens,
+                          void *stream);
+
+/* kda_attn_decode — attention of the last K tokens (1: a decode step; more: K draft rows) of each of
+ * N sequences over their cached rows, which include those K tokens' own. With heads a multiple of kv_heads,
+ * query head h reads kv head h / (heads / kv_heads). Row t of a sequence of length len stands at
+ * position p = len - K + t and sees the cached rows
+ *     j <= p   and   (window == 0  or  j > p - window  or  j < sinks)
+ *     o = sum_j a_j v_j,  a = softmax_j(scale q.k_j),  lse = ln sum_j exp(scale q.k_j)
+ * A row that sees nothing (an empty slot, say) gives o = 0 and lse = -inf.
+ *   q      [N * K, heads, head_dim] BF16, rows n K .. n K + K - 1 of sequence n;  out likewise (output)
+ *   lse    [N * K, heads] F32 output, or NULL
+ *   slots  DEVICE int32 [N] or NULL (slot n); a slot may be listed more than once
+ *   dims   heads, head_dim (the cache's) and scale (the score scale, e.g. 1/sqrt(head_dim))
+ *   window 0 (none) or >= 1, the query's own token counted;  sinks >= 0
+ *   scratch  at least kda_attn_decode_scratch_bytes(N, K, dims, cache) bytes, 16-byte aligned: partial
+ *          results of cache ranges that several CTAs share; contents on entry do not matter
+ * heads / kv_heads * K <= 64 (else KDA_ERR_UNSUPPORTED: use kda_attn_prefill). The rows of a
+ * sequence with a slot out of range or a length that is negative or past max_pages pages are left
+ * unwritten, and so are those of (sequence, kv head) pairs that need a table entry that is no
+ * page; each latches KDA_ERR_INVALID_ARG. Table entries wholly outside the window may be anything. What
+ * pages hold past seq_len, or outside the window of all K rows, has no effect, NaN included; V
+ * rows that some of the K rows see must be finite. */
+KDA_API int kda_attn_decode(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *slots, int N, int K,
+                            int window, int sinks, kda_bf16 *out, float *lse, void *scratch, size_t scratch_bytes,
+                            const kda_dims *dims, void *stream);
+
+/* Scratch bytes of kda_attn_decode on the current device (0 if N or K is 0 or the sizes are refused). */
+KDA_API size_t kda_attn_decode_scratch_bytes(int N, int K, const kda_dims *dims, const kda_kv_cache *cache);
+
+/* kda_attn_prefill — the same attention for packed rows: the n_i query rows of sequence i (rows
+ * [cu_seqlens[i], cu_seqlens[i+1])) are the last n_i tokens of slot slots[i], so row t stands at position
+ * seq_len - n_i + t (a whole prompt, a chunk of one behind cached tokens, or draft rows).
+ *   q, out      [total_tokens, heads, head_dim] BF16;  lse [total_tokens, heads] F32 or NULL
+ *   cu_seqlens  DEVICE int32 [B + 1];  slots  DEVICE int32 [B] or NULL (slot i); a slot may be listed more than once
+ *   max_rows    at least n_i for every sequence
+ *   other arguments as kda_attn_decode
+ * Rows at or past cu_seqlens[B] are left as they were. A sequence with bad bounds (negative, decreasing,
+ * past total_tokens, or longer than max_rows), a slot out of range or a length that is negative or past
+ * max_pages pages is left unwritten, and so are the rows of a query tile that needs a table entry
+ * that is no page; each latches KDA_ERR_INVALID_ARG. What pages hold past seq_len, or outside the
+ * window of all rows of a query tile, has no effect; V rows that a row of the call sees must be finite. */
+KDA_API int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *cu_seqlens,
+                             const int *slots, int B, int max_rows, int total_tokens, int window, int sinks,
+                             kda_bf16 *out, float *lse, const kda_dims *dims, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

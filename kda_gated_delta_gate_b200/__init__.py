@@ -44,6 +44,13 @@ class KdaBlockWeights(ctypes.Structure):
                [("hidden", ctypes.c_int), ("rank", ctypes.c_int)]
 
 
+class KdaKvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "page_table", "seq_len", "ref", "scratch")] + \
+               [("layer_stride", ctypes.c_longlong)] + \
+               [(n, ctypes.c_int) for n in ("layers", "num_pages", "page_size", "kv_heads", "head_dim", "max_seqs",
+                                            "max_pages")]
+
+
 # workspace stage buffers (include/kda.h, KDA_BUF_*)
 BUFFERS = ("qkv_proj", "conv_out", "q_f32", "k_f32", "v_f32", "gate", "beta", "core", "g_raw", "out_gate",
            "o_norm_out", "final_out", "f_a_out", "g_a_out", "prefill_scratch")
@@ -53,6 +60,7 @@ _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _DIMS = ctypes.POINTER(KdaDims)
+_KV = ctypes.POINTER(KdaKvCache)
 
 _SIGS = {
     "kda_version": ([], _I),
@@ -103,6 +111,15 @@ _SIGS = {
     "kda_block_prefill_batched": ([_VP, _VP, _I, _I, _VP, _VP, _VP, _VP], _I),
     "kda_block_verify": ([_VP, _VP, _VP, _I, _I, _VP, _VP, _VP, ctypes.c_size_t, _VP, _VP], _I),
     "kda_block_verify_fold": ([_VP, _VP, _I, _I, _VP, _VP, _VP, _VP, _VP], _I),
+    "kda_kv_scratch_bytes": ([_I, _I], ctypes.c_size_t),
+    "kda_kv_reserve": ([_KV, _VP, _VP, _I, _VP], _I),
+    "kda_kv_fork": ([_KV, _VP, _VP, _I, _VP], _I),
+    "kda_kv_truncate": ([_KV, _VP, _VP, _I, _VP], _I),
+    "kda_kv_compact": ([_KV, _VP, _VP], _I),
+    "kda_kv_append": ([_KV, _I, _VP, _VP, ctypes.c_longlong, _VP, _VP, _I, _I, _VP], _I),
+    "kda_attn_decode": ([_KV, _I, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, ctypes.c_size_t, _DIMS, _VP], _I),
+    "kda_attn_decode_scratch_bytes": ([_I, _I, _DIMS, _KV], ctypes.c_size_t),
+    "kda_attn_prefill": ([_KV, _I, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _DIMS, _VP], _I),
 }
 
 
@@ -532,3 +549,113 @@ def kda_block_decode_graph(weights: KdaBlockWeights, hidden, N: int, h_state_ptr
     _call("kda_block_decode_graph", ctypes.byref(weights), _p(hidden), N, _p(h_state_ptrs), _p(conv_state_ptrs),
           ws.handle, ctypes.byref(h))
     return Graph(h)
+
+
+class KVCache:
+    """A paged key-value cache over the caller's device tensors (include/kda.h, kda_kv_cache):
+    k, v [layers, num_pages, kv_heads, page_size, head_dim] BF16 (a pool each; the layers may be a
+    strided view), page_table [max_seqs, max_pages], seq_len [max_seqs] and ref [num_pages] int32.
+    KVCache.empty allocates them. The tensors stay the caller's to read; the object keeps them alive."""
+
+    def __init__(self, k, v, page_table, seq_len, ref):
+        import torch
+        for name, t, nd, dt in (("k", k, 5, torch.bfloat16), ("v", v, 5, torch.bfloat16),
+                                ("page_table", page_table, 2, torch.int32), ("seq_len", seq_len, 1, torch.int32),
+                                ("ref", ref, 1, torch.int32)):
+            if t.dim() != nd or t.dtype != dt or t.device != k.device:
+                raise ValueError(f"{name}: a {nd}-D {dt} tensor on {k.device} is wanted, not {t.dim()}-D {t.dtype} "
+                                 f"on {t.device}")
+            inner = t[0] if nd == 5 and t.shape[0] else t
+            if not inner.is_contiguous():
+                raise ValueError(f"{name} must be contiguous{' within a layer' if nd == 5 else ''}")
+        if k.shape != v.shape or (k.shape[0] > 1 and k.stride(0) != v.stride(0)):
+            raise ValueError("k and v must have one shape and one layer stride")
+        if ref.numel() != k.shape[1] or seq_len.numel() != page_table.shape[0]:
+            raise ValueError("ref has one entry per page, seq_len one per row of page_table")
+        self.k, self.v, self.page_table, self.seq_len, self.ref = k, v, page_table, seq_len, ref
+        layers, num_pages, kv_heads, page_size, head_dim = k.shape
+        max_seqs, max_pages = page_table.shape
+        nb = int(lib().kda_kv_scratch_bytes(num_pages, max_seqs))
+        self.scratch = torch.empty(max(nb, 16), dtype=torch.uint8, device=k.device)
+        self.struct = KdaKvCache(_p(k), _p(v), _p(page_table), _p(seq_len), _p(ref), _p(self.scratch),
+                                 k.stride(0) if layers > 1 else k[0].numel() if layers else 0, layers, num_pages,
+                                 page_size, kv_heads, head_dim, max_seqs, max_pages)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, max_seqs: int, max_pages: int,
+              layers: int = 1, device="cuda"):
+        """A cache with every page free and every slot empty (the pools are left uninitialised)."""
+        import torch
+        shape = (layers, num_pages, kv_heads, page_size, head_dim)
+        return cls(torch.empty(shape, dtype=torch.bfloat16, device=device),
+                   torch.empty(shape, dtype=torch.bfloat16, device=device),
+                   torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(max_seqs, dtype=torch.int32, device=device),
+                   torch.zeros(num_pages, dtype=torch.int32, device=device))
+
+
+def kda_kv_reserve(cache: KVCache, slots, add, n: int, stream=None):
+    """Room for add[i] more tokens in slot slots[i] (device int32 [n]; slots None: slot i)."""
+    return _call("kda_kv_reserve", ctypes.byref(cache.struct), _p(slots), _p(add), n, _stream(stream))
+
+
+def kda_kv_fork(cache: KVCache, parent, child, n: int, stream=None):
+    """Slot child[i] becomes a copy of slot parent[i]: full pages shared, a partly filled last page copied."""
+    return _call("kda_kv_fork", ctypes.byref(cache.struct), _p(parent), _p(child), n, _stream(stream))
+
+
+def kda_kv_truncate(cache: KVCache, slots, new_len, n: int, stream=None):
+    """Slot slots[i] keeps its first new_len[i] tokens (0 frees it)."""
+    return _call("kda_kv_truncate", ctypes.byref(cache.struct), _p(slots), _p(new_len), n, _stream(stream))
+
+
+def kda_kv_compact(cache: KVCache, live=None, stream=None):
+    """Move the live pages to the front of the pools; live (device int32 [1]) receives their number."""
+    return _call("kda_kv_compact", ctypes.byref(cache.struct), _p(live), _stream(stream))
+
+
+def _rows_stride(name, k_new, v_new) -> int:
+    ld = k_new.stride(0)
+    if k_new.stride(-1) != 1 or v_new.stride(-1) != 1 or (v_new.shape[0] > 1 and v_new.stride(0) != ld):
+        raise ValueError(f"{name}: k_new and v_new are rows of contiguous values with one row stride")
+    if k_new.dim() == 3 and (k_new.stride(1) != k_new.shape[2] or v_new.stride(1) != v_new.shape[2]):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return ld
+
+
+def kda_kv_append(cache: KVCache, layer: int, k_new, v_new, cu_seqlens, slots, B: int, total_tokens: int,
+                  stream=None):
+    """Packed new K and V rows ([total_tokens, kv_heads * head_dim] or [total_tokens, kv_heads, head_dim], any row
+    stride) into the pages of their sequences, whose last tokens they are."""
+    return _call("kda_kv_append", ctypes.byref(cache.struct), layer, _p(k_new), _p(v_new),
+                 _rows_stride("kda_kv_append", k_new, v_new), _p(cu_seqlens), _p(slots), B, total_tokens,
+                 _stream(stream))
+
+
+def kda_attn_decode_scratch_bytes(N: int, K: int, d: KdaDims, cache: KVCache) -> int:
+    return int(lib().kda_attn_decode_scratch_bytes(N, K, ctypes.byref(d), ctypes.byref(cache.struct)))
+
+
+def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d: KdaDims, window: int = 0,
+                    sinks: int = 0, lse=None, stream=None, scratch=None):
+    """Attention of the last K tokens of each of N sequences over the cache (q, out [N*K, heads, head_dim] BF16,
+    lse [N*K, heads] F32 or None). `scratch`: the stream's cached buffer when None; while the current stream is
+    being captured a buffer of the graph's own, so that graphs captured one after the other may run at once."""
+    import torch
+    st = _stream(stream)
+    if scratch is None:
+        need = kda_attn_decode_scratch_bytes(N, K, d, cache)
+        if torch.cuda.is_current_stream_capturing():
+            scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=cache.k.device)
+        else:
+            scratch = scratch_buffer(need, cache.k.device, st)
+    return _call("kda_attn_decode", ctypes.byref(cache.struct), layer, _p(q), _p(slots), N, K, window, sinks, _p(out),
+                 _p(lse), _p(scratch), scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
+
+
+def kda_attn_prefill(cache: KVCache, layer: int, q, cu_seqlens, slots, B: int, max_rows: int, total_tokens: int, out,
+                     d: KdaDims, window: int = 0, sinks: int = 0, lse=None, stream=None):
+    """Attention of packed rows, the last tokens of their sequences, over the cache (q, out
+    [total_tokens, heads, head_dim] BF16, lse [total_tokens, heads] F32 or None)."""
+    return _call("kda_attn_prefill", ctypes.byref(cache.struct), layer, _p(q), _p(cu_seqlens), _p(slots), B, max_rows,
+                 total_tokens, window, sinks, _p(out), _p(lse), ctypes.byref(d), _stream(stream))

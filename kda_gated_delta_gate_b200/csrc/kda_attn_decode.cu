@@ -1,0 +1,575 @@
+// Attention of the last K tokens of N sequences over their paged cache (include/kda.h, kda_attn_decode).
+//
+// Per (sequence, kv head): S = scale q k^T over the visible rows, o = softmax(S) v, in one pass with
+// the running maximum m and sum l of the softmax (base 2): p = 2^(s - m), l += sum p, o = o 2^(m_old - m) + p v.
+// The G K query rows of a kv head (G query heads per kv head) share every K and V row read, so the pass
+// moves 4 D bytes per cached row and head for 4 G K D flops: HBM bounds it.
+//
+// Split: the visible 64-row tiles of all (sequence, kv head) pairs form one list; each CTA of a fixed
+// grid (the resident CTAs of the card) takes an equal run of it, whatever the mix of lengths. A pair that
+// falls into one run is finished there; a pair that runs cut leaves (m, l, o) per CTA in scratch, and
+// join_kernel, one block per cut and row, adds the parts in run order (the same bits on every call).
+//
+// A CTA is four warps over one tile: K and V rows arrive by 16-byte cp.async, two or three tiles
+// ahead, in shared memory whose 16-byte chunks are permuted by chunk ^ (row % 8); mma.sync (m16n8k16, BF16 in,
+// FP32 sums) takes K by ldmatrix and V by ldmatrix.trans. With at most 16 query rows each warp takes 16 of the
+// tile's 64 keys and its own m, l and o, joined at the pair's end; with up to 32 two warps share a key half, with
+// up to 64 each warp has 16 rows and all keys. mma.sync is enough: at 16 rows the products need about a sixth of its
+// rate while HBM is saturated. p is rounded to BF16 for the second product (half a step, 2^-9 of each weight, below
+// the BF16 output's own rounding); l sums the unrounded p.
+#include <algorithm>
+
+#include "kv.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kTile = 64;      // cached rows per tile
+constexpr int kThreads = 128;  // four warps
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct DecodeArgs {
+    KvView c;
+    const uint16_t *q;
+    const int *slots;
+    uint16_t *out;
+    float *lse;
+    float *part_o, *part_ml;  // [CTA][2][rows][D], [CTA][2][rows][2]
+    long long *info;          // [0] all tiles; then per CTA: pair (n * kv_heads + h), first tile of the pair, tiles of it
+    int *status;
+    int N, K, G, heads, window, sinks;
+    float scale2;  // scale * log2(e)
+};
+
+// The tiles of one sequence: `sink` leading ones, then those from `lo / 64` to the last.
+struct Span {
+    int len, lo, sink, tiles;  // tiles = 0: the sequence is skipped
+};
+__device__ __forceinline__ Span span_of(const DecodeArgs &a, int n, bool &bad) {
+    Span s{0, 0, 0, 0};
+    const int slot = a.slots ? a.slots[n] : n;
+    bad = true;
+    if (slot < 0 || slot >= a.c.max_seqs) return s;
+    const int len = a.c.len[slot];
+    if (len < 0 || len > a.c.max_pages * a.c.page_size) return s;
+    bad = false;
+    s.len = len;
+    s.lo = a.window ? max(0, len - a.K - a.window + 1) : 0;
+    if (s.lo > 0) s.sink = min((min(a.sinks, s.lo) + kTile - 1) / kTile, s.lo / kTile);
+    s.tiles = max(1, s.sink + (len + kTile - 1) / kTile - s.lo / kTile);  // an empty one still writes its zeros
+    return s;
+}
+__device__ __forceinline__ int tile_row0(const Span &s, int i) {
+    return (i < s.sink ? i : i - s.sink + s.lo / kTile) * kTile;
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool fill) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// Tile runs: CTA c of `ctas` takes tiles [run_start(c), run_start(c + 1)).
+__device__ __forceinline__ long long run_start(long long tiles, int ctas, int c) { return tiles * c / ctas; }
+
+template <int D, int MT>
+struct DecodeCfg {
+    static constexpr int KG = 4 / MT;             // key groups: warps that split a tile's keys
+    static constexpr int KPW = kTile / KG;        // keys of a tile per warp
+    static constexpr int STAGES = D == 64 ? 4 : (MT == 4 ? 2 : 3);
+    static constexpr int HALF = kTile * D * 2;    // bytes of a tile's K (or V)
+    static constexpr int ROWS = 16 * MT;
+    static constexpr int OFF_O = STAGES * 2 * HALF;            // [ROWS][D] FP32
+    static constexpr int OFF_ML = OFF_O + ROWS * D * 4;        // [KG][ROWS][2]
+    static constexpr int OFF_MISC = OFF_ML + KG * ROWS * 8;    // scan, cursor, flags
+    static constexpr int BYTES = OFF_MISC + 256;
+    static constexpr int CTAS = D == 64 ? (MT == 4 ? 2 : 3) : 2;  // resident per SM
+};
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using C = DecodeCfg<D, MT>;
+    extern __shared__ __align__(128) uint8_t sm[];
+    float *const so = reinterpret_cast<float *>(sm + C::OFF_O);
+    float2 *const sml = reinterpret_cast<float2 *>(sm + C::OFF_ML);
+    long long *const sscan = reinterpret_cast<long long *>(sm + C::OFF_MISC);  // 4 warp sums
+    long long *const scur = sscan + 4;                                         // sequence, its first tile
+    int *const sbad = reinterpret_cast<int *>(scur + 2);                       // per stage: a needed entry is no page
+
+    grid_release();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hk = a.c.kv_heads, rows = a.G * a.K;
+
+    // ---- this CTA's run: the tiles of all sequences, summed by the whole block
+    const int per = (a.N + kThreads - 1) / kThreads, n_lo = min(a.N, tid * per), n_hi = min(a.N, n_lo + per);
+    long long mine = 0;
+    for (int n = n_lo; n < n_hi; ++n) {
+        bool bad;
+        mine += span_of(a, n, bad).tiles;
+        if (bad && blockIdx.x == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+    }
+    mine *= hk;
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sscan[warp] = x;
+    __syncthreads();
+    long long base = x - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w < warp) base += sscan[w];
+        all += sscan[w];
+    }
+    const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), all));
+    const int cta = blockIdx.x;
+    if (cta == 0 && tid == 0) a.info[0] = all;
+    if (cta >= ctas) return;
+    const long long t_begin = run_start(all, ctas, cta), t_end = run_start(all, ctas, cta + 1);
+    if (t_begin >= base && t_begin < base + mine) {
+        long long at = base;
+        for (int n = n_lo; n < n_hi; ++n) {
+            bool bad;
+            const long long w = static_cast<long long>(span_of(a, n, bad).tiles) * hk;
+            if (t_begin < at + w) {
+                scur[0] = n;
+                scur[1] = at;
+                break;
+            }
+            at += w;
+        }
+    }
+    __syncthreads();
+
+    // ---- cursors over (sequence, kv head, tile of the pair); both start at t_begin
+    struct Cursor {
+        int n, h, i;  // sequence, kv head, tile within the pair
+        Span s;
+        const int *table;
+    };
+    auto open = [&](Cursor &c) {  // the sequence's span; skips sequences without tiles
+        bool bad;
+        for (; c.n < a.N; ++c.n) {
+            c.s = span_of(a, c.n, bad);
+            if (c.s.tiles > 0) break;
+        }
+        if (c.n < a.N) c.table = a.c.table + static_cast<size_t>(a.slots ? a.slots[c.n] : c.n) * a.c.max_pages;
+    };
+    auto step = [&](Cursor &c) {
+        if (++c.i < c.s.tiles) return;
+        c.i = 0;
+        if (++c.h < hk) return;
+        c.h = 0;
+        ++c.n;
+        open(c);
+    };
+    Cursor lc;
+    lc.n = static_cast<int>(scur[0]);
+    lc.h = 0;
+    lc.i = 0;
+    open(lc);
+    {
+        const long long in = t_begin - scur[1];
+        lc.h = static_cast<int>(in / lc.s.tiles);
+        lc.i = static_cast<int>(in - static_cast<long long>(lc.h) * lc.s.tiles);
+    }
+    Cursor cc = lc;
+    if (tid == 0) {
+        long long *const f = a.info + 1 + 3 * static_cast<long long>(cta);
+        f[0] = static_cast<long long>(lc.n) * hk + lc.h;
+        f[1] = t_begin - lc.i;
+        f[2] = lc.s.tiles;
+    }
+
+    // ---- loads: each lane l < 64 / page keeps the table entry of the tile's l-th page, one tile ahead
+    const int ents = a.c.page_size >= kTile ? 1 : kTile >> a.c.page_shift;
+    auto entry_of = [&](const Cursor &c) {
+        int e = 0;
+        if (lane < ents && c.n < a.N) {
+            const int j = tile_row0(c.s, c.i) + lane * a.c.page_size;
+            if (j < c.s.len) e = __ldg(c.table + (j >> a.c.page_shift));
+        }
+        return e;
+    };
+    long long tl = t_begin;  // tiles requested so far
+    int entry = entry_of(lc);
+    auto load = [&](int stage) {
+        if (tl < t_end) {
+            const int j0 = tile_row0(lc.s, lc.i);
+            const uint32_t sk = smem_addr(sm + stage * 2 * C::HALF), sv = sk + C::HALF;
+            constexpr int CH = D / 8, RP = kThreads / CH;  // 16-byte chunks per row, rows per pass
+            const int ch = tid % CH;
+            // a page that some visible row of the tile needs and that is none: every warp finds the same
+            const int jp = j0 + lane * a.c.page_size, je = min(min(jp + a.c.page_size, j0 + kTile), lc.s.len);
+            const bool wrong = __any_sync(0xffffffffu, lane < ents && jp < lc.s.len && (je > lc.s.lo || jp < a.sinks) &&
+                                                           (entry < 0 || entry >= a.c.num_pages));
+            if (tid == 0) sbad[stage] = wrong;
+#pragma unroll
+            for (int r0 = 0; r0 < kTile; r0 += RP) {
+                const int r = r0 + tid / CH, j = j0 + r;
+                const int pg = __shfl_sync(0xffffffffu, entry, ents == 1 ? 0 : r >> a.c.page_shift);
+                // rows that no query row sees are zeros in shared memory, whatever the page holds
+                const bool live = j < lc.s.len && (j >= lc.s.lo || j < a.sinks) && pg >= 0 && pg < a.c.num_pages;
+                const size_t off = live ? ((static_cast<size_t>(pg) * hk + lc.h) * a.c.page_size + (j & (a.c.page_size - 1))) * D + 8 * ch
+                                        : 0;
+                const uint32_t so16 = static_cast<uint32_t>(r * D * 2 + ((ch ^ (r & 7)) << 4));
+                cp16(sk + so16, a.c.k + off, live);
+                cp16(sv + so16, a.c.v + off, live);
+            }
+            step(lc);
+            ++tl;
+            entry = entry_of(lc);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    // ---- per warp: rows 16 mt .., keys KPW kg ..
+    const int mt = warp % MT, kg = warp / MT;
+    const int ra = 16 * mt + (lane >> 2), rb = ra + 8;  // this thread's two rows
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4], m[2], l[2];
+    int pos[2];
+    bool seg_bad = false;
+    auto begin_pair = [&]() {
+        const uint16_t *const qn = a.q + (static_cast<size_t>(cc.n) * a.K * a.heads + static_cast<size_t>(cc.h) * a.G) * D;
+        const int ta = ra / a.G, tb = rb / a.G;
+        const uint16_t *const qa = qn + (static_cast<size_t>(ta) * a.heads + (ra - ta * a.G)) * D + 2 * (lane & 3);
+        const uint16_t *const qb = qn + (static_cast<size_t>(tb) * a.heads + (rb - tb * a.G)) * D + 2 * (lane & 3);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            qf[ks][0] = ra < rows ? __ldg(reinterpret_cast<const uint32_t *>(qa + 16 * ks)) : 0u;
+            qf[ks][1] = rb < rows ? __ldg(reinterpret_cast<const uint32_t *>(qb + 16 * ks)) : 0u;
+            qf[ks][2] = ra < rows ? __ldg(reinterpret_cast<const uint32_t *>(qa + 16 * ks + 8)) : 0u;
+            qf[ks][3] = rb < rows ? __ldg(reinterpret_cast<const uint32_t *>(qb + 16 * ks + 8)) : 0u;
+        }
+        pos[0] = cc.s.len - a.K + min(ta, a.K - 1);
+        pos[1] = cc.s.len - a.K + min(tb, a.K - 1);
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+        seg_bad = false;
+    };
+
+#pragma unroll 1
+    for (int s = 0; s < C::STAGES - 1; ++s) load(s);
+    int stage = 0;
+    long long seg0 = t_begin;  // where the current pair's tiles in this run begin
+    begin_pair();
+#pragma unroll 1
+    for (long long t = t_begin; t < t_end; ++t) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 2) : "memory");
+        __syncthreads();  // tile t has landed for every thread, and the stage before it is free
+        const bool tile_bad = sbad[stage] != 0;
+        load(stage == 0 ? C::STAGES - 1 : stage - 1);
+        seg_bad |= tile_bad;
+
+        const int j0 = tile_row0(cc.s, cc.i) + C::KPW * kg;
+        const uint32_t sk = smem_addr(sm + stage * 2 * C::HALF), sv = sk + C::HALF;
+        float s[C::KPW / 8][4];
+#pragma unroll
+        for (int nb = 0; nb < C::KPW / 16; ++nb) {
+            float(&s0)[4] = s[2 * nb], (&s1)[4] = s[2 * nb + 1];
+            s0[0] = s0[1] = s0[2] = s0[3] = s1[0] = s1[1] = s1[2] = s1[3] = 0.f;
+            // matrices: keys +0..7 / +8..15 (lane bit 4), channels +0..7 / +8..15 (lane bit 3)
+            const int r = C::KPW * kg + 16 * nb + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const int ch = 2 * ks + ((lane >> 3) & 1);
+                uint32_t b[4];
+                ldsm4(sk + r * D * 2 + ((ch ^ (r & 7)) << 4), b);
+                mma16816(s0, qf[ks], b[0], b[1]);
+                mma16816(s1, qf[ks], b[2], b[3]);
+            }
+        }
+        // the whole tile is visible to every row, or each weight is looked at
+        const bool all_seen = j0 + C::KPW <= cc.s.len - a.K + 1 && (!a.window || j0 > cc.s.len - 1 - a.window);
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int nb = 0; nb < C::KPW / 8; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float y = s[nb][e] * a.scale2;
+                if (!all_seen) {
+                    const int j = j0 + 8 * nb + 2 * (lane & 3) + (e & 1), p = pos[e >> 1];
+                    const bool seen = j <= p && (!a.window || j > p - a.window || j < a.sinks);
+                    y = seen ? y : -INFINITY;
+                }
+                s[nb][e] = y;
+                top[e >> 1] = fmaxf(top[e >> 1], y);
+            }
+        }
+        float safe[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+            const float mn = fmaxf(m[e], top[e]);
+            safe[e] = mn == -INFINITY ? 0.f : mn;
+            const float f = ex2(m[e] - safe[e]);
+            m[e] = mn;
+            l[e] *= f;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+                o[d][2 * e] *= f;
+                o[d][2 * e + 1] *= f;
+            }
+        }
+#pragma unroll
+        for (int nb = 0; nb < C::KPW / 8; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[nb][e] = ex2(s[nb][e] - safe[e >> 1]);
+                l[e >> 1] += s[nb][e];
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < C::KPW / 16; ++kb) {
+            const uint32_t p[4] = {pack_bf16(s[2 * kb][0], s[2 * kb][1]), pack_bf16(s[2 * kb][2], s[2 * kb][3]),
+                                   pack_bf16(s[2 * kb + 1][0], s[2 * kb + 1][1]),
+                                   pack_bf16(s[2 * kb + 1][2], s[2 * kb + 1][3])};
+            const int r = C::KPW * kg + 16 * kb + (lane & 15);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                const int ch = 2 * d + (lane >> 4);
+                uint32_t b[4];
+                ldsm4t(sv + r * D * 2 + ((ch ^ (r & 7)) << 4), b);
+                mma16816(o[2 * d], p, b[0], b[1]);
+                mma16816(o[2 * d + 1], p, b[2], b[3]);
+            }
+        }
+        if (++stage == C::STAGES) stage = 0;
+
+        // ---- the pair's last tile of this run: join the warps, then write the result or this run's part
+        if (cc.i + 1 == cc.s.tiles || t + 1 == t_end) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+                if ((lane & 3) == 0) sml[kg * C::ROWS + (e ? rb : ra)] = make_float2(m[e], l[e]);
+            }
+            __syncthreads();
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float top_all = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < C::KG; ++g) top_all = fmaxf(top_all, sml[g * C::ROWS + (e ? rb : ra)].x);
+                f[e] = ex2(m[e] - (top_all == -INFINITY ? 0.f : top_all));
+            }
+#pragma unroll
+            for (int g = 0; g < C::KG; ++g) {
+                if (kg == g) {
+#pragma unroll
+                    for (int d = 0; d < D / 8; ++d) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float2 *const w = reinterpret_cast<float2 *>(so + (e ? rb : ra) * D + 8 * d + 2 * (lane & 3));
+                            float2 v = make_float2(o[d][2 * e] * f[e], o[d][2 * e + 1] * f[e]);
+                            if (g) {
+                                const float2 u = *w;
+                                v.x += u.x;
+                                v.y += u.y;
+                            }
+                            *w = v;
+                        }
+                    }
+                }
+                __syncthreads();
+            }
+            const long long pair0 = t - cc.i;  // the pair's first tile in the list
+            const bool whole = pair0 >= t_begin && cc.i + 1 == cc.s.tiles;
+            const int slot = seg0 == t_begin ? 0 : 1;
+            for (int i = tid; i < rows * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), d = 4 * (i % (D / 4));
+                float top_all = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int g = 0; g < C::KG; ++g) top_all = fmaxf(top_all, sml[g * C::ROWS + r].x);
+                const float ref = top_all == -INFINITY ? 0.f : top_all;
+#pragma unroll
+                for (int g = 0; g < C::KG; ++g) sum += sml[g * C::ROWS + r].y * ex2(sml[g * C::ROWS + r].x - ref);
+                const float4 v = *reinterpret_cast<const float4 *>(so + r * D + d);
+                if (whole) {
+                    if (!seg_bad) {
+                        const int tk = r / a.G;
+                        const size_t row = (static_cast<size_t>(cc.n) * a.K + tk) * a.heads + cc.h * a.G + (r - tk * a.G);
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        *reinterpret_cast<uint2 *>(a.out + row * D + d) =
+                            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+                        if (a.lse && d == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top_all + log2f(sum)) * kLn2;
+                    }
+                } else {
+                    const size_t pr = (static_cast<size_t>(cta) * 2 + slot) * rows + r;
+                    *reinterpret_cast<float4 *>(a.part_o + pr * D + d) = v;
+                    if (d == 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * pr) = make_float2(top_all, seg_bad ? -1.f : sum);
+                }
+            }
+            if (seg_bad && tid == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+            __syncthreads();  // so and sml are read; the next pair may overwrite them
+            if (t + 1 < t_end) {
+                step(cc);
+                seg0 = t + 1;
+                begin_pair();
+            }
+        } else {
+            ++cc.i;
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Block (c - 1, r): row r of the pair that the cut between runs c - 1 and c splits, if it is the pair's first cut.
+template <int D>
+__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeArgs a, int grid_ctas) {
+    __shared__ float sw[D / 32];
+    grid_acquire();
+    const long long all = a.info[0];
+    const int ctas = static_cast<int>(min(static_cast<long long>(grid_ctas), all));
+    const int c = blockIdx.x + 1, r = blockIdx.y, rows = a.G * a.K, tid = threadIdx.x;
+    if (c >= ctas) return;
+    const long long *const f = a.info + 1 + 3LL * c;
+    const long long pair = f[0], first = f[1], tiles = f[2];
+    if (run_start(all, ctas, c) == first || run_start(all, ctas, c - 1) > first) return;
+    int last = c;
+    while (last + 1 < ctas && run_start(all, ctas, last + 1) < first + tiles) ++last;
+    const int slot0 = run_start(all, ctas, c - 1) == first ? 0 : 1;
+    auto at = [&](int k) { return (static_cast<size_t>(k) * 2 + (k == c - 1 ? slot0 : 0)) * rows + r; };
+
+    // the largest m of the parts, and whether one of them met a bad page
+    float top = -INFINITY;
+    bool bad = false;
+    for (int k = c - 1 + tid; k <= last; k += D) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at(k));
+        top = fmaxf(top, ml.x);
+        bad |= ml.y == -1.f;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((tid & 31) == 0) sw[tid >> 5] = top;
+    if (__syncthreads_or(bad)) return;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) top = fmaxf(top, sw[w]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, v = 0.f;
+#pragma unroll 4
+    for (int k = c - 1; k <= last; ++k) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at(k));
+        const float w = ex2(ml.x - ref);
+        sum = fmaf(ml.y, w, sum);
+        v = fmaf(a.part_o[at(k) * D + tid], w, v);
+    }
+    const int n = static_cast<int>(pair / a.c.kv_heads), h = static_cast<int>(pair - static_cast<long long>(n) * a.c.kv_heads);
+    const int tk = r / a.G;
+    const size_t row = (static_cast<size_t>(n) * a.K + tk) * a.heads + h * a.G + (r - tk * a.G);
+    a.out[row * D + tid] = f32_to_bf16(sum == 0.f ? 0.f : v / sum);
+    if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+template <int D, int MT>
+int launch_decode(const DecodeArgs &a, int grid, cudaStream_t s) {
+    using C = DecodeCfg<D, MT>;
+    static std::atomic<unsigned long long> attr{0};
+    KDA_TRY(smem_opt_in(decode_kernel<D, MT>, C::BYTES, attr, true));
+    decode_kernel<D, MT><<<grid, kThreads, C::BYTES, s>>>(a);
+    KDA_TRY(launch_status());
+    if (grid < 2) return KDA_OK;
+    return launch_after(join_kernel<D>, dim3(grid - 1, a.G * a.K), dim3(D), 0, s, a, grid);
+}
+
+int ctas_per_sm(int D, int mt) { return D == 64 ? (mt == 4 ? 2 : 3) : 2; }
+int m_tiles(int rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
+
+int check_shape(int N, int K, const kda_dims *dims, const kda_kv_cache *cache) {
+    KDA_TRY(check_cache(cache));
+    KDA_TRY(check_dims(dims));
+    if (N < 0 || K < 0) return KDA_ERR_INVALID_ARG;
+    if (dims->head_dim != cache->head_dim || dims->heads % cache->kv_heads) return KDA_ERR_INVALID_ARG;
+    if (static_cast<long long>(dims->heads / cache->kv_heads) * K > 64) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(N) * K > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+size_t info_bytes(int grid) { return (1 + 3 * static_cast<size_t>(grid)) * 8 / 16 * 16 + 16; }
+
+}  // namespace
+}  // namespace kda
+
+extern "C" {
+
+size_t kda_attn_decode_scratch_bytes(int N, int K, const kda_dims *dims, const kda_kv_cache *cache) {
+    if (kda::check_shape(N, K, dims, cache) != KDA_OK || N == 0 || K == 0) return 0;
+    const size_t rows = static_cast<size_t>(dims->heads / cache->kv_heads) * K;
+    const int grid = kda::ctas_per_sm(dims->head_dim, kda::m_tiles(static_cast<int>(rows))) * kda::num_sms();
+    return kda::info_bytes(grid) + static_cast<size_t>(grid) * 2 * rows * (dims->head_dim + 4) * sizeof(float);
+}
+
+int kda_attn_decode(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *slots, int N, int K, int window,
+                    int sinks, kda_bf16 *out, float *lse, void *scratch, size_t scratch_bytes, const kda_dims *dims,
+                    void *stream) {
+    KDA_TRY(kda::check_shape(N, K, dims, cache));
+    if (!q || !out || window < 0 || sinks < 0 || layer < 0 || layer >= cache->layers) return KDA_ERR_INVALID_ARG;
+    if (!kda::aligned16(q) || !kda::aligned16(out)) return KDA_ERR_MISALIGNED;
+    if (N == 0 || K == 0) return KDA_OK;
+    if (!scratch) return KDA_ERR_INVALID_ARG;
+    if (!kda::aligned16(scratch)) return KDA_ERR_MISALIGNED;
+    if (scratch_bytes < kda_attn_decode_scratch_bytes(N, K, dims, cache)) return KDA_ERR_CAPACITY;
+    kda::DecodeArgs a{};
+    a.c = kda::kv_view(cache, layer);
+    a.q = q;
+    a.slots = slots;
+    a.out = out;
+    a.lse = lse;
+    a.status = kda::device_status_ptr();
+    if (!a.status) return KDA_ERR_CUDA;
+    a.N = N;
+    a.K = K;
+    a.G = dims->heads / cache->kv_heads;
+    a.heads = dims->heads;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale2 = dims->scale * kda::kLog2e;
+    const int rows = a.G * K, mt = kda::m_tiles(rows), D = dims->head_dim;
+    const int grid = kda::ctas_per_sm(D, mt) * kda::num_sms();
+    char *const p = static_cast<char *>(scratch);
+    a.info = reinterpret_cast<long long *>(p);
+    a.part_o = reinterpret_cast<float *>(p + kda::info_bytes(grid));
+    a.part_ml = a.part_o + static_cast<size_t>(grid) * 2 * rows * D;
+    auto s = static_cast<cudaStream_t>(stream);
+    if (D == 128)
+        return mt == 1   ? kda::launch_decode<128, 1>(a, grid, s)
+               : mt == 2 ? kda::launch_decode<128, 2>(a, grid, s)
+                         : kda::launch_decode<128, 4>(a, grid, s);
+    return mt == 1   ? kda::launch_decode<64, 1>(a, grid, s)
+           : mt == 2 ? kda::launch_decode<64, 2>(a, grid, s)
+                     : kda::launch_decode<64, 4>(a, grid, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,70 @@
+// Shared by the paged key-value cache calls (kda_kv.cu) and the attention over it (kda_attn_*.cu). Internal.
+#pragma once
+
+#include "common.cuh"
+
+namespace kda {
+
+// Host checks of a cache struct: sizes within the int arithmetic of the kernels, pools aligned.
+inline int check_cache(const kda_kv_cache *c) {
+    if (!c || !c->k || !c->v || !c->page_table || !c->seq_len || !c->ref) return KDA_ERR_INVALID_ARG;
+    if (c->layers < 1 || c->num_pages < 1 || c->kv_heads < 1 || c->max_seqs < 1 || c->max_pages < 1)
+        return KDA_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return KDA_ERR_UNSUPPORTED;
+    const int ps = c->page_size;
+    if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return KDA_ERR_UNSUPPORTED;
+    // pool rows, table entries and positions are ints
+    const long long rows = static_cast<long long>(c->num_pages) * c->kv_heads * ps;
+    if (rows > 0x7fffffffLL || static_cast<long long>(c->num_pages) * c->kv_heads > 0x7fffffffLL / ps ||
+        static_cast<long long>(c->max_pages) * ps > 0x7fffffffLL - 4096 ||
+        static_cast<long long>(c->max_seqs) * c->max_pages > 0x7fffffffLL || c->kv_heads > 65535)
+        return KDA_ERR_UNSUPPORTED;
+    if (c->layers > 1 && c->layer_stride < rows * c->head_dim) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || (c->layers > 1 && c->layer_stride % 8)) return KDA_ERR_MISALIGNED;
+    return KDA_OK;
+}
+
+// The cache as the kernels see it; k and v at the layer of the call.
+struct KvView {
+    uint16_t *k, *v;
+    int *table, *len, *ref;
+    int num_pages, page_size, page_shift, kv_heads, max_seqs, max_pages;
+};
+
+inline KvView kv_view(const kda_kv_cache *c, int layer) {
+    KvView w;
+    w.k = c->k + static_cast<long long>(layer) * c->layer_stride;
+    w.v = c->v + static_cast<long long>(layer) * c->layer_stride;
+    w.table = c->page_table;
+    w.len = c->seq_len;
+    w.ref = c->ref;
+    w.num_pages = c->num_pages;
+    w.page_size = c->page_size;
+    w.page_shift = __builtin_ctz(static_cast<unsigned>(c->page_size));
+    w.kv_heads = c->kv_heads;
+    w.max_seqs = c->max_seqs;
+    w.max_pages = c->max_pages;
+    return w;
+}
+
+// Programmatic dependent launch: let the next grid start; wait until the grids before have completed.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_acquire() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch `kernel` so that it may start while the grid before it on the stream still runs (it waits in grid_acquire).
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace kda

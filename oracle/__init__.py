@@ -308,3 +308,31 @@ def block_decode(W, hidden_rows, h_state, conv_state, *, scale: float = 1.0, l2_
     r.update(qkv_proj=x_rows, g_raw=g_raw, b_logit=b_logit, out_gate=out_gate,
              final_out=bf16_round(linear(r["o_norm_out"], W.o_proj)))
     return r
+
+
+def attention(q, k, v, q_pos, scale: float, window: int = 0, sinks: int = 0):
+    """Softmax attention of query rows at positions q_pos over the cached rows 0 .. L-1 of one sequence
+    (the attention mixer that a hybrid stack puts beside the KDA block), one kv head.
+
+    q [n, D], k and v [L, D], q_pos [n]. Row i sees j <= q_pos[i] with window == 0 or
+    j > q_pos[i] - window or j < sinks. Returns (o [n, D], lse [n], spread [n, D]) with spread =
+    sum_j a_j |v_j|, the scale of what rounding the weights can move o by. Rows that see nothing:
+    o = 0, lse = -inf.
+    """
+    q, k, v = _f64(q), _f64(k), _f64(v)
+    n, L = q.shape[0], k.shape[0]
+    o, lse, spread = np.zeros_like(q), np.full(n, -np.inf), np.zeros_like(q)
+    for i in range(n):
+        p = int(q_pos[i])
+        seen = np.arange(min(p + 1, L)) if p >= 0 else np.arange(0)
+        if window:
+            seen = seen[(seen > p - window) | (seen < sinks)]
+        if not len(seen):
+            continue
+        x = scale * (k[seen] @ q[i])
+        top = x.max()
+        w = np.exp(x - top)
+        lse[i] = top + np.log(w.sum())
+        w /= w.sum()
+        o[i], spread[i] = w @ v[seen], w @ np.abs(v[seen])
+    return o, lse, spread

@@ -1,0 +1,173 @@
+"""kda_attn_decode against the FP64 oracle: lengths from none to long ones, odd head groups, windows
+and sinks, pages of every size, hidden rows that hold NaN, refusals, and calls side by side."""
+import numpy as np
+import pytest
+import torch
+
+import kda_gated_delta_gate_b200 as kda
+from tests.attn_harness import Case, check, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _status(cuda_ok):
+    kda.device_status(clear=True)
+    yield
+    assert kda.device_status(clear=True) == 0
+
+
+def run(c, K, **kw):
+    out = torch.full((len(c.order) * K, c.heads, c.dim), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((len(c.order) * K, c.heads), float("nan"), device="cuda")
+    kda.kda_attn_decode(c.cache, c.layer, c.qd, kw.pop("slots", i32(c.order)), len(c.order), K, out, c.d, window=c.window,
+                        sinks=c.sinks, lse=lse, **kw)
+    return out, lse
+
+
+# lengths, K, heads, kv_heads, dim, page, window, sinks
+CASES = [
+    ([0, 1, 15, 16, 17, 63, 64, 65, 200], 1, 4, 2, 64, 16, 0, 0),
+    ([0, 1, 2, 127, 128, 129], 1, 6, 6, 128, 32, 0, 0),
+    ([1000], 1, 8, 1, 128, 64, 0, 0),
+    ([700, 3, 0, 321], 1, 10, 2, 128, 128, 0, 0),
+    ([515, 64], 1, 32, 2, 64, 256, 0, 0),
+    ([0, 1, 2, 3, 100, 777], 3, 4, 2, 128, 16, 0, 0),   # fewer tokens than rows among them
+    ([300, 5, 64], 4, 10, 2, 128, 64, 0, 0),             # 20 rows per kv head
+    ([300, 5, 64, 129], 4, 32, 2, 128, 16, 0, 0),        # 64
+    ([300, 5, 64, 129], 8, 16, 2, 64, 32, 0, 0),
+    ([257, 31], 2, 48, 3, 64, 16, 0, 0),
+    ([0, 1, 40, 300, 641], 1, 4, 2, 64, 16, 1, 0),
+    ([0, 1, 40, 300, 641], 1, 4, 2, 128, 16, 7, 1),
+    ([10, 64, 300, 641], 1, 4, 2, 64, 32, 64, 4),
+    ([10, 64, 300, 641], 3, 6, 2, 128, 16, 100, 5),
+    ([10, 190, 300, 641], 2, 4, 1, 64, 64, 33, 70),
+    ([10, 190, 300, 1641], 1, 4, 1, 128, 128, 130, 200),
+    ([500, 600], 1, 4, 1, 128, 256, 5000, 3),            # a window longer than the cache
+]
+
+
+@pytest.mark.parametrize("lens,K,heads,kv_heads,dim,page,window,sinks", CASES)
+def test_matches_the_oracle(lens, K, heads, kv_heads, dim, page, window, sinks):
+    c = Case(lens, [K] * len(lens), heads, kv_heads, dim, page, window, sinks, seed=len(lens) + dim)
+    check(*run(c, K), c.expected())
+
+
+def test_one_long_sequence_beside_short_ones():
+    c = Case([3, 40000, 0, 777, 64], [1] * 5, 4, 2, 128, 16, seed=2)
+    out, lse = run(c, 1)
+    check(out, lse, c.expected())
+    for _ in range(3):  # the parts are added in one order
+        again = run(c, 1)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_many_sequences_more_than_threads():
+    lens = [(i * 29) % 150 for i in range(300)]
+    c = Case(lens, [1] * 300, 4, 2, 64, 16, seed=9)
+    check(*run(c, 1), c.expected())
+
+
+def test_layers_slots_and_optional_arguments():
+    c = Case([70, 130, 33], [2] * 3, 4, 2, 64, 16, layers=3, layer=1, order=[2, 0, 2, 1], seed=4)
+    out, lse = run(c, 2)
+    check(out, lse, c.expected())
+    c = Case([70, 130, 33], [2] * 3, 4, 2, 64, 16, layers=2, layer=1, seed=4)
+    out, lse = run(c, 2, slots=None)
+    check(out, lse, c.expected())
+    out2 = torch.empty_like(out)
+    kda.kda_attn_decode(c.cache, 1, c.qd, None, 3, 2, out2, c.d)
+    assert torch.equal(out, out2)
+
+
+@pytest.mark.parametrize("evicted", [-1, -2 ** 31, 10 ** 9])
+def test_pages_that_left_the_window_are_not_looked_at(evicted):
+    c = Case([900, 640, 300], [1] * 3, 4, 2, 128, 16, 64, 20, evicted=evicted, seed=6)
+    check(*run(c, 1), c.expected())
+
+
+def test_bad_slots_lengths_and_pages_leave_their_rows():
+    c = Case([700, 130, 64, 90, 200], [1] * 5, 4, 2, 64, 16, seed=11)
+    o = c.expected()
+    c.cache.seq_len[3] = -5
+    c.cache.page_table[0, 20] = 10 ** 8
+    c.cache.seq_len[4] = 10 ** 9
+    slots = i32([0, 1, 2, 3, 4])
+    out, lse = run(c, 1, slots=slots)
+    assert kda.device_status(clear=True) == 1
+    assert torch.isnan(out[[0, 3, 4]]).all() and torch.isnan(lse[[0, 3, 4]]).all()
+    check(out[1:3], lse[1:3], tuple(x[1:3] for x in o))
+    out, lse = run(c, 1, slots=i32([1, -1, 2, 5, 2 ** 31 - 1]))
+    assert kda.device_status(clear=True) == 1
+    assert torch.isnan(out[[1, 3, 4]]).all()
+    out, lse = run(c, 1, slots=i32([-1] * 5))
+    assert kda.device_status(clear=True) == 1 and torch.isnan(out).all()
+
+
+def test_far_pages():
+    """Rows past the 2^32nd element of a pool."""
+    pages = 2 ** 32 // (8 * 64 * 128) + 40
+    cache = kda.KVCache.empty(pages, 64, 8, 128, 2, 30)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    far = torch.arange(pages - 30, pages, device="cuda")
+    for t in (cache.k, cache.v):
+        t[0, far] = torch.randn((30, 8, 64, 128), generator=gen, device="cuda").bfloat16()
+    cache.page_table[1] = far.int()
+    cache.seq_len[1] = 1900
+    near = kda.KVCache(cache.k[:, far].contiguous(), cache.v[:, far].contiguous(),
+                       torch.arange(30, dtype=torch.int32, device="cuda")[None], i32([1900]), i32([1] * 30))
+    q = torch.randn((1, 16, 128), generator=gen, device="cuda").bfloat16()
+    d, a, b = kda.dims(16, 128, scale=0.09), torch.empty_like(q), torch.empty_like(q)
+    kda.kda_attn_decode(cache, 0, q, i32([1]), 1, 1, a, d)
+    kda.kda_attn_decode(near, 0, q, None, 1, 1, b, d)
+    assert torch.equal(a, b) and a.float().abs().sum() > 0
+
+
+def test_streams_graphs_and_guard_bands():
+    """Two streams at once, two graphs replayed at once, and outputs inside canaries."""
+    cs = [Case([900, 31, 2000], [1] * 3, 8, 2, 128, 16, seed=s) for s in (1, 2)]
+    want = [c.expected() for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    outs = [None, None]
+    for _ in range(5):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(s):
+                outs[i] = run(c, 1)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        check(*o, w)
+    graphs, held = [], []
+    for c in cs:
+        out, lse = torch.zeros_like(c.qd), torch.zeros((3, 8), device="cuda")
+        slots = i32(c.order)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kda.kda_attn_decode(c.cache, 0, c.qd, slots, 3, 1, out, c.d, lse=lse)
+        graphs.append(g)
+        held.append((out, lse, slots))
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (out, lse, _), w in zip(held, want):
+        check(out, lse, w)
+    c, M = cs[0], 4096
+    n = kda.kda_attn_decode_scratch_bytes(3, 1, c.d, c.cache)
+    raw = [torch.full((2 * M + b,), 0xA5, dtype=torch.uint8, device="cuda") for b in (c.qd.numel() * 2, 3 * 8 * 4, n)]
+    out = raw[0][M:-M].view(torch.bfloat16).view(c.qd.shape)
+    lse = raw[1][M:-M].view(torch.float32).view(3, 8)
+    kda.kda_attn_decode(c.cache, 0, c.qd, None, 3, 1, out, c.d, lse=lse, scratch=raw[2][M:-M])
+    check(out, lse, want[0])
+    for r in raw:
+        assert (r[:M] == 0xA5).all() and (r[-M:] == 0xA5).all()
+
+
+def test_extreme_scores():
+    """Scores far apart and large: nothing overflows on the way, and one weight takes all."""
+    c = Case([400, 77], [1, 1], 4, 2, 64, 16, spread=2000.0, seed=8)
+    out, lse = run(c, 1)
+    o, l, _ = c.expected()
+    assert torch.isfinite(out).all()
+    assert np.allclose(lse.double().cpu().numpy(), l, rtol=2.0 ** -17, atol=0)

@@ -1,0 +1,171 @@
+"""The paged key-value cache's bookkeeping and row writing against tests/kv_model.py: every array
+and every page bit for bit, over random sequences of calls and the cases that a call refuses."""
+import numpy as np
+import pytest
+import torch
+
+import kda_gated_delta_gate_b200 as kda
+from tests.kv_model import KvModel
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _status(cuda_ok):
+    kda.device_status(clear=True)
+    yield
+    assert kda.device_status(clear=True) == 0
+
+
+def _i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device="cuda")
+
+
+def _bits(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+class Pair:
+    """A cache on the GPU and its model, kept in step."""
+
+    def __init__(self, pages=40, page=16, heads=2, dim=64, seqs=8, max_pages=12, layers=2, seed=0):
+        self.cache = kda.KVCache.empty(pages, page, heads, dim, seqs, max_pages, layers)
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        for t in (self.cache.k, self.cache.v):
+            t.copy_(torch.randn(t.shape, generator=gen, device="cuda"))
+        self.rng = np.random.default_rng(seed)
+        c = self.cache
+        self.model = KvModel(_bits(c.k), _bits(c.v), c.page_table.cpu().numpy(), c.seq_len.cpu().numpy(),
+                             c.ref.cpu().numpy())
+
+    def call(self, name, *args):
+        c, n = self.cache, len(args[0]) if args else 0
+        if name == "compact":
+            live = torch.full((1,), -7, dtype=torch.int32, device="cuda")
+            kda.kda_kv_compact(c, live)
+            assert int(live) == self.model.compact()
+        else:
+            getattr(kda, "kda_kv_" + name)(c, *[_i32(a) for a in args], n)
+            getattr(self.model, name)(*args)
+        self.check()
+
+    def append(self, layer, slots, rows, ids=True):
+        c, total = self.cache, sum(rows)
+        w = c.k.shape[2] * c.k.shape[4]
+        wide = torch.from_numpy(self.rng.standard_normal((total + 3, 3 * w), dtype=np.float32)).cuda().bfloat16()
+        k_new, v_new = wide[:, w:2 * w], wide[:, 2 * w:]
+        cu = np.concatenate([[0], np.cumsum(rows)])
+        kda.kda_kv_append(c, layer, k_new, v_new, _i32(cu), _i32(slots) if ids else None, len(rows), total + 3)
+        shape = (-1, c.k.shape[2], c.k.shape[4])
+        self.model.append(layer, _bits(k_new).reshape(shape), _bits(v_new).reshape(shape), cu, slots)
+        self.check()
+
+    def check(self):
+        c, m = self.cache, self.model
+        assert kda.device_status(clear=True) == m.status
+        m.status = 0
+        assert np.array_equal(c.seq_len.cpu().numpy(), m.seq_len)
+        assert np.array_equal(c.ref.cpu().numpy(), m.ref)
+        assert np.array_equal(c.page_table.cpu().numpy(), m.table)
+        assert np.array_equal(_bits(c.k), m.k) and np.array_equal(_bits(c.v), m.v)
+
+
+@pytest.mark.parametrize("page,dim,heads,layers", [(16, 64, 2, 2), (32, 128, 1, 1), (64, 128, 3, 1), (128, 64, 1, 2),
+                                                     (256, 64, 1, 1)])
+def test_random_calls_match_the_model(page, dim, heads, layers):
+    p = Pair(pages=30, page=page, heads=heads, dim=dim, seqs=7, max_pages=9, layers=layers, seed=page)
+    rng = p.rng
+    for _ in range(40):
+        m = p.model
+        op = rng.choice(["reserve", "reserve", "fork", "truncate", "compact", "append"])
+        n = int(rng.integers(1, 6))
+        slots = [int(x) for x in rng.choice(np.arange(-1, 8), n)]  # out of range and repeated ones among them
+        if op == "reserve":
+            p.call(op, slots, [int(x) for x in rng.choice([0, 1, 5, page - 1, page, 2 * page + 3, 5 * page], n)])
+        elif op == "fork":
+            p.call(op, [int(x) for x in rng.integers(0, 7, n)], slots)
+        elif op == "truncate":
+            lens = [int(rng.integers(-1 if rng.random() < .05 else 0, m.seq_len[s] + 1)) if 0 <= s < 7 else 0 for s in slots]
+            p.call(op, slots, [0 if rng.random() < .3 else x for x in lens])
+        elif op == "compact":
+            p.call(op)
+        else:
+            slots = [int(x) for x in rng.permutation(7)[:n]]
+            p.append(int(rng.integers(layers)), slots, [int(rng.integers(0, min(4, m.seq_len[s]) + 1)) for s in slots])
+
+
+def test_reserve_without_slot_list_and_out_of_pages():
+    p = Pair(pages=10, page=16, seqs=4, max_pages=8)
+    kda.kda_kv_reserve(p.cache, None, _i32([16, 17, 64, 5]), 4)  # 1 + 2 + 4 + 1 pages
+    p.model.reserve([0, 1, 2, 3], [16, 17, 64, 5])
+    p.check()
+    p.call("reserve", [0, 1, 2, 3], [1, 15, 17, 11])  # 1, 0, 2, 0: the third passes the two free pages
+    p.call("reserve", [3, 2, 1], [129, 0, 0])         # past max_pages: refused, the rest as asked
+    p.call("truncate", [1, 2], [3, 0])
+    p.call("compact")
+
+
+def test_fork_takes_parents_as_they_stand_and_refuses_what_is_not_empty():
+    p = Pair(pages=40, page=16, seqs=8)
+    p.call("reserve", [0, 1], [37, 32])
+    p.append(0, [0], [37])
+    p.append(1, [1], [32])
+    p.call("fork", [0, 0, 1, 3, 0, 2], [2, 3, 4, 5, 2, 6])  # 3 -> 5 and 2 -> 6: empty at the start; 2 listed twice
+    p.call("fork", [0, 7, 9, 0], [1, 7, 6, -1])             # not empty, itself, no slot
+    p.call("reserve", [0, 2, 3], [1, 1, 12])
+    p.append(1, [2, 3], [1, 12])
+    p.call("truncate", [0, 2, 4], [0, 0, 0])
+    p.call("truncate", [3, 1], [20, 10])
+    p.call("fork", [3, 3], [0, 2])
+    p.call("truncate", [0, 2], [12, 3])       # into shared pages
+    p.call("reserve", [0, 3, 2], [1, 1, 20])  # copies of their own
+    p.append(0, [0, 3, 2], [1, 1, 20])
+
+
+def test_append_edges():
+    p = Pair(pages=30, page=16, seqs=6, max_pages=5)
+    p.call("reserve", [0, 1, 2, 3], [40, 1, 0, 16])
+    p.append(0, [3, 0, 1, 2], [16, 40, 1, 0])
+    p.append(1, [0, 1, 0, 9], [3, 1, 2, 1])      # listed before, no slot: refused
+    p.append(1, [1, 3], [2, 1])                   # more rows than tokens: refused
+    p.append(0, [0, 1], [7, 1], ids=False)
+    p.call("fork", [0], [4])
+    p.append(0, [0], [30])                        # its first rows lie in pages that slot 4 shares: not written
+    for cu in ([5, 3, 4], [0, -4, 2], [0, 2, 99], [2 ** 31 - 1, -2 ** 31, 3]):  # no bounds: nothing is read or written outside
+        before = p.cache.k.clone()
+        rows = torch.zeros((4, 128), dtype=torch.bfloat16, device="cuda")
+        kda.kda_kv_append(p.cache, 0, rows, rows, _i32(cu), _i32([5, 5]), 2, 4)
+        kda.device_status(clear=True)
+        assert torch.equal(p.cache.k, before)
+
+
+def test_large_pools_and_many_slots():
+    """More pages than one round of the scan, more pairs than one block has threads, far offsets: pages
+    past the 2^32nd byte of a pool."""
+    pages, seqs = 33000, 1500
+    c = kda.KVCache.empty(pages, 64, 8, 128, seqs, 40)
+    add = [(37 * i) % 1300 for i in range(seqs)]
+    kda.kda_kv_reserve(c, None, _i32(add), seqs)
+    need = [-(-a // 64) for a in add]
+    assert kda.device_status() == 0 and c.seq_len.tolist() == add
+    table, first = c.page_table.cpu().numpy(), np.concatenate([[0], np.cumsum(need)])
+    for i in range(seqs):
+        assert table[i, :need[i]].tolist() == list(range(first[i], first[i + 1])) and (table[i, need[i]:] == -1).all()
+    # all but the last slots leave; what remains moves down from the far end
+    kda.kda_kv_reserve(c, _i32([0]), _i32([2500 - add[0]]), 1)
+    full = int((c.ref > 0).sum())
+    keep = _i32(range(1400, 1500))
+    probe = torch.randn((1, 8 * 128), device="cuda").bfloat16()
+    last = int(c.page_table[0, 39])
+    assert last == full - 1
+    c.ref[last], c.ref[pages - 1] = 0, 1
+    c.page_table[0, 39] = pages - 1
+    kda.kda_kv_append(c, 0, probe, -probe, _i32([0, 1]), _i32([0]), 1, 1)
+    assert torch.equal(c.k[0, pages - 1, :, 3].reshape(-1), probe[0])  # token 2499: row 3 of its page
+    kda.kda_kv_truncate(c, _i32(range(1, 1400)), _i32([0] * 1399), 1399)
+    live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_kv_compact(c, live)
+    assert int(live) == 40 + sum(need[1400:]) == int((c.ref[:int(live)] > 0).sum()) == int((c.ref > 0).sum())
+    got = c.page_table[0, 39]
+    assert torch.equal(c.k[0, got, :, 3].reshape(-1), probe[0]) and torch.equal(c.v[0, got, :, 3].reshape(-1), -probe[0])
+    assert int(c.page_table.max()) == int(live) - 1 and len(keep) == 100

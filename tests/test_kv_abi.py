@@ -1,0 +1,121 @@
+"""The paged cache's and its attention's argument checks, on the host: nothing here reaches a device."""
+import ctypes
+
+import pytest
+import torch
+
+import kda_gated_delta_gate_b200 as kda
+
+BOGUS = 0x10000
+
+
+@pytest.fixture(scope="module")
+def L():
+    from kda_gated_delta_gate_b200 import build
+    build.build()
+    return kda.lib()
+
+
+def _c(**kw):
+    f = dict(k=BOGUS, v=BOGUS, page_table=BOGUS, seq_len=BOGUS, ref=BOGUS, scratch=BOGUS, layer_stride=1 << 20, layers=2,
+             num_pages=64, page_size=16, kv_heads=2, head_dim=64, max_seqs=4, max_pages=8)
+    f.update(kw)
+    return ctypes.byref(kda.KdaKvCache(*[f[n] for n, _ in kda.KdaKvCache._fields_]))
+
+
+BAD_CACHES = [(dict(k=None), 1), (dict(v=None), 1), (dict(page_table=None), 1), (dict(seq_len=None), 1), (dict(ref=None), 1),
+              (dict(k=BOGUS + 8), 7), (dict(v=BOGUS + 2), 7), (dict(layers=0), 1), (dict(num_pages=0), 1),
+              (dict(page_size=8), 4), (dict(page_size=48), 4), (dict(page_size=512), 4), (dict(head_dim=96), 4),
+              (dict(kv_heads=0), 1), (dict(max_seqs=0), 1), (dict(max_pages=-1), 1), (dict(num_pages=1 << 27), 4),
+              (dict(max_pages=1 << 28), 4), (dict(layer_stride=64 * 2 * 16 * 64 - 8), 1), (dict(layer_stride=(1 << 20) + 4), 7)]
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_every_call_refuses_a_bad_cache(L, kw, code):
+    c, d = _c(**kw), ctypes.byref(kda.dims(4, kw.get("head_dim", 64)))
+    assert L.kda_kv_reserve(c, BOGUS, BOGUS, 1, None) == code
+    assert L.kda_kv_fork(c, BOGUS, BOGUS, 1, None) == code
+    assert L.kda_kv_truncate(c, BOGUS, BOGUS, 1, None) == code
+    assert L.kda_kv_compact(c, None, None) == code
+    assert L.kda_kv_append(c, 0, BOGUS, BOGUS, 128, BOGUS, BOGUS, 1, 1, None) == code
+    assert L.kda_attn_decode(c, 0, BOGUS, None, 1, 1, 0, 0, BOGUS, None, BOGUS, 1 << 30, d, None) == code
+    assert L.kda_attn_prefill(c, 0, BOGUS, BOGUS, None, 1, 1, 1, 0, 0, BOGUS, None, d, None) == code
+    assert L.kda_attn_decode_scratch_bytes(1, 1, d, c) == 0
+
+
+def test_bookkeeping_arguments(L):
+    assert L.kda_kv_scratch_bytes(0, 4) == 0 and L.kda_kv_scratch_bytes(4, 0) == 0
+    assert L.kda_kv_scratch_bytes(64, 4) >= 4 * (4 * 64 + 4 * 4)
+    for f, two in ((L.kda_kv_reserve, 1), (L.kda_kv_fork, 0), (L.kda_kv_truncate, 1)):
+        assert f(_c(), BOGUS, None, 1, None) == 1
+        assert f(_c(), BOGUS, BOGUS, -1, None) == 1
+        assert f(_c(), BOGUS, BOGUS, 5, None) == 1  # more than max_seqs
+        assert f(_c(), BOGUS, BOGUS, 0, None) == 0
+        assert f(None, BOGUS, BOGUS, 1, None) == 1
+    assert L.kda_kv_fork(_c(), None, BOGUS, 1, None) == 1
+    assert L.kda_kv_reserve(_c(scratch=None), BOGUS, BOGUS, 1, None) == 1
+    assert L.kda_kv_compact(_c(scratch=BOGUS + 4), None, None) == 7
+
+
+def test_append_arguments(L):
+    f = L.kda_kv_append
+    assert f(_c(), 2, BOGUS, BOGUS, 128, BOGUS, None, 1, 1, None) == 1      # layer
+    assert f(_c(), -1, BOGUS, BOGUS, 128, BOGUS, None, 1, 1, None) == 1
+    assert f(_c(), 0, None, BOGUS, 128, BOGUS, None, 1, 1, None) == 1
+    assert f(_c(), 0, BOGUS, BOGUS, 128, None, None, 1, 1, None) == 1
+    assert f(_c(), 0, BOGUS, BOGUS, 120, BOGUS, None, 1, 1, None) == 1      # rows would overlap
+    assert f(_c(), 0, BOGUS, BOGUS, 132, BOGUS, None, 1, 1, None) == 7
+    assert f(_c(), 0, BOGUS + 8, BOGUS, 128, BOGUS, None, 1, 1, None) == 7
+    assert f(_c(), 0, BOGUS, BOGUS, 128, BOGUS, None, -1, 1, None) == 1
+    assert f(_c(), 0, BOGUS, BOGUS, 128, BOGUS, None, 0, 1, None) == 0
+    assert f(_c(), 0, BOGUS, BOGUS, 128, BOGUS, None, 1, 0, None) == 0
+
+
+def test_attention_arguments(L):
+    d = kda.dims(4, 64)
+    dp = ctypes.byref(d)
+
+    def dec(c=None, layer=0, q=BOGUS, N=1, K=1, w=0, s=0, out=BOGUS, scr=BOGUS, nb=1 << 30, dims=dp):
+        return L.kda_attn_decode(c or _c(), layer, q, None, N, K, w, s, out, None, scr, nb, dims, None)
+
+    def pre(c=None, layer=0, q=BOGUS, cu=BOGUS, B=1, rows=1, total=1, w=0, s=0, out=BOGUS, dims=dp):
+        return L.kda_attn_prefill(c or _c(), layer, q, cu, None, B, rows, total, w, s, out, None, dims, None)
+
+    for f in (dec, pre):
+        assert f(layer=2) == 1 and f(layer=-1) == 1 and f(q=None) == 1 and f(out=None) == 1
+        assert f(w=-1) == 1 and f(s=-1) == 1 and f(q=BOGUS + 8) == 7 and f(out=BOGUS + 4) == 7
+        assert f(dims=None) == 1
+        assert f(dims=ctypes.byref(kda.dims(5, 64))) == 1    # heads not a multiple of kv_heads
+        assert f(dims=ctypes.byref(kda.dims(4, 128))) == 1   # not the cache's head_dim
+        assert f(dims=ctypes.byref(kda.dims(4, 32))) == 4
+    assert dec(N=-1) == 1 and dec(K=-1) == 1 and dec(N=0) == 0 and dec(K=0) == 0
+    assert dec(K=33) == 4 and dec(dims=ctypes.byref(kda.dims(130, 64))) == 4  # more than 64 rows per kv head
+    need = L.kda_attn_decode_scratch_bytes(1, 1, dp, _c())
+    assert need > 0 and L.kda_attn_decode_scratch_bytes(0, 1, dp, _c()) == 0
+    assert dec(scr=None) == 1 and dec(scr=BOGUS + 8) == 7 and dec(nb=need - 16) == 3
+    assert pre(cu=None) == 1 and pre(B=-1) == 1 and pre(rows=-1) == 1 and pre(total=-1) == 1
+    assert pre(B=0) == 0 and pre(total=0) == 0 and pre(rows=0) == 1 and pre(B=70000) == 4
+
+
+def test_cache_object_checks_its_tensors(L):
+    def make(**kw):
+        t = dict(k=torch.zeros(2, 4, 2, 16, 64, dtype=torch.bfloat16), v=torch.zeros(2, 4, 2, 16, 64, dtype=torch.bfloat16),
+                 page_table=torch.zeros(3, 5, dtype=torch.int32), seq_len=torch.zeros(3, dtype=torch.int32),
+                 ref=torch.zeros(4, dtype=torch.int32))
+        t.update(kw)
+        return kda.KVCache(**t)
+
+    c = make().struct
+    assert (c.layers, c.num_pages, c.kv_heads, c.page_size, c.head_dim, c.max_seqs, c.max_pages) == (2, 4, 2, 16, 64, 3, 5)
+    assert c.layer_stride == 4 * 2 * 16 * 64
+    wide = torch.zeros(2, 6, 2, 16, 64, dtype=torch.bfloat16)[:, :4]  # layers further apart than a pool is long
+    assert make(k=wide, v=wide).struct.layer_stride == 6 * 2 * 16 * 64
+    for kw in (dict(k=torch.zeros(2, 4, 2, 16, 64)), dict(v=torch.zeros(2, 4, 2, 16, 32, dtype=torch.bfloat16)),
+               dict(ref=torch.zeros(5, dtype=torch.int32)), dict(seq_len=torch.zeros(3, dtype=torch.int64)),
+               dict(page_table=torch.zeros(5, 3, dtype=torch.int32).T), dict(k=torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)),
+               dict(v=torch.zeros(2, 4, 16, 2, 64, dtype=torch.bfloat16).transpose(2, 3))):
+        with pytest.raises(ValueError):
+            make(**kw)
+    with pytest.raises(ValueError):
+        kda._rows_stride("append", torch.zeros(4, 8).T, torch.zeros(4, 8).T)
+    assert kda._rows_stride("append", torch.zeros(4, 24)[:, 8:16], torch.zeros(4, 24)[:, 16:]) == 24
