@@ -745,7 +745,8 @@ KDA_API size_t kda_attn_decode_scratch_bytes(int N, int K, const kda_dims *dims,
  *   max_rows    at least n_i for every sequence
  *   other arguments as kda_attn_decode
  * Rows at or past cu_seqlens[B] are left as they were. A sequence with bad bounds (negative, decreasing,
- * past total_tokens, or longer than max_rows), a slot out of range or a length that is negative or past
+ * past total_tokens, or longer than max_rows; where cu_seqlens decreases, its other sequences
+ * too), a slot out of range or a length that is negative or past
  * max_pages pages is left unwritten, and so are the rows of a query tile that needs a table entry
  * that is no page; each latches KDA_ERR_INVALID_ARG. What pages hold past seq_len, or outside the
  * window of all rows of a query tile, has no effect; V rows that a row of the call sees must be finite. */

@@ -1,56 +1,470 @@
 // Attention of packed query rows over their paged cache (include/kda.h, kda_attn_prefill).
+//
+// Per (sequence, kv head) the n query tokens of G query heads are n G rows (token major, then head), cut into
+// tiles of 256; a CTA takes one such tile and walks the visible 128-row tiles of the cache once, with the
+// softmax's running reference m and sum l: S = Q K^T, P = 2^(scale log2(e) S - m), l += rowsum P, O += P V.
+// 4 D flops and one exponential per (row, cached row) pair: the tensor cores bound it at D = 128 (2 x 512
+// cycles of MMA per 128 x 128 x 128 pair of products against 1024 cycles of exponentials), the exponentials at D = 64.
+//
+// Twelve warps, one CTA per SM (the softmax warps take registers that the other warpgroup gives up: 384 x 168 =
+// 256 x 208 + 128 x 88):
+//   warps 0..3, 4..7  softmax of the tile's rows 0..127 and 128..255 (one row per thread, so that no
+//                     shuffles are needed): S from TMEM, mask at the edges, P as BF16 back into the columns
+//                     of S; also Q into shared memory at the start and O out at the end
+//   warp 8            TMA: K and V tiles page by page (one box of 64 channels per page, at most 128 rows),
+//                     128-byte swizzle, two stages each
+//   warp 9            tcgen05.mma: S_a, S_b; then per cache tile P_a V, next S_a, P_b V, next S_b, so that one half's
+//                     products run under the other half's softmax; P is the A operand from TMEM
+// O is rescaled only when a row's maximum has grown by more than 2^8 since its reference was set (P then
+// stays below 2^8, harmless in BF16 and FP32); a commit of S_x(i) also covers P_x(i - 1) V, so O needs no barrier of its own.
+// TMEM columns: S_a 0, S_b 128, O_a 256, O_b 384. P is rounded to BF16 for the second product (half a
+// step, 2^-9 of each weight, below the BF16 output's own rounding); l sums the unrounded P.
+//
+// Rows of a cache tile that no row of the CTA sees (past the last token, before the window, pages that
+// left the table) are not loaded where they fill a page, and their V rows are zeroed in shared memory: what
+// they hold cannot reach a result. Every wait is bounded; one that gives up latches KDA_ERR_TIMEOUT.
+#include <algorithm>
+#include <cmath>
+
 #include "kv.cuh"
+#include "tma.cuh"
+#include "umma.cuh"
 
 namespace kda {
 namespace {
 
-// One warp per (row, head): an online softmax over the visible rows, lanes along the channels.
+using namespace umma;
+
+constexpr int kRows = 256, kKeys = 128, kPrefillThreads = 384;
+constexpr long long kPrefillWait = 4000000000LL;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.0f;  // log2 of how far a maximum may outgrow its reference
+
+struct PrefillArgs {
+    CUtensorMap tk, tv;
+    KvView c;
+    const uint16_t *q;
+    const int *cu, *slots;
+    uint16_t *out;
+    float *lse;
+    int *status;
+    int B, max_rows, total, heads, G, window, sinks, nslots;
+    float scale2;  // |scale| log2(e)
+    uint32_t flip;  // sign bits of a BF16 pair if scale < 0 (the queries are negated), else 0
+};
+
 template <int D>
-__global__ void __launch_bounds__(128) prefill_kernel(const KvView c, const uint16_t *q, const int *cu, const int *slots,
-                                                      int B, int max_rows, int total, int heads, int window, int sinks,
-                                                      float scale, uint16_t *out, float *lse, int *status) {
-    constexpr int E = D / 32;
-    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int c0 = cu[b], c1 = cu[b + 1], s = slots ? slots[b] : b, n = c1 - c0;
-    int len = 0;
-    bool ok = c0 >= 0 && c1 >= c0 && c1 <= total && n <= max_rows && s >= 0 && s < c.max_seqs;
-    if (ok) len = c.len[s];
-    ok = ok && len >= 0 && len <= c.max_pages * c.page_size;
-    if (!ok) {
-        if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) atomicExch(status, KDA_ERR_INVALID_ARG);
-        return;
-    }
-    if (t >= n) return;
-    const int p = len - n + t, hkv = h / (heads / c.kv_heads);
-    const size_t row = static_cast<size_t>(c0 + t) * heads + h;
-    float qv[E], o[E], m = -INFINITY, l = 0.f;
+struct PrefillCfg {
+    static constexpr int TILE = kKeys * D * 2;  // bytes of a Q half, K or V tile
+    static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + 2 * TILE, OFF_BARS = OFF_V + 2 * TILE;
+    static constexpr int BYTES = OFF_BARS + 256 + 1024;
+};
+
+__device__ __forceinline__ void tma_load_2d(void *smem_dst, const CUtensorMap *tm, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] . B[smem]: A's rows are TMEM lanes, two BF16 values of K per column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
 #pragma unroll
-    for (int e = 0; e < E; ++e) qv[e] = bf16_to_f32(q[row * D + lane + 32 * e]), o[e] = 0.f;
-    const int lo = window ? max(0, p - window + 1) : 0;
-    for (int j = (lo > 0 && sinks > 0) ? 0 : lo; j <= p; ++j) {
-        if (j < lo && j >= sinks) { j = lo - 1; continue; }
-        const int pg = c.table[static_cast<size_t>(s) * c.max_pages + (j >> c.page_shift)];
-        if (pg < 0 || pg >= c.num_pages) {
-            if (lane == 0) atomicExch(status, KDA_ERR_INVALID_ARG);
-            return;
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
+    const uint32_t addr = smem_u32(bar);
+    if (mbar_try_wait(addr, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(addr, parity)) {
+        if (*abort) return false;
+        if (clock64() - t0 > kPrefillWait) {
+            *abort = 1;
+            atomicExch(status, KDA_ERR_TIMEOUT);
+            return false;
         }
-        const size_t off = ((static_cast<size_t>(pg) * c.kv_heads + hkv) * c.page_size + (j & (c.page_size - 1))) * D + lane;
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) x = fmaf(qv[e], bf16_to_f32(c.k[off + 32 * e]), x);
-#pragma unroll
-        for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-        x *= scale;
-        const float mn = fmaxf(m, x), f = expf(m - mn), w = expf(x - mn);
-        m = mn;
-        l = l * f + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * bf16_to_f32(c.v[off + 32 * e]);
     }
+    return true;
+}
+
+// Where a CTA's rows stand: the sequence's length and rows, and per half the positions and cache tiles.
+struct Tile {
+    int b, slot, c0, n, len, r0;  // r0: first of the 256 rows (token * G + head)
+    int lo, hi;                   // visible cached rows: [lo, hi) and those below `sinks`
+    int sink;                     // leading tiles that only sinks need
+    int tiles[2];                 // per half
+};
+__device__ __forceinline__ int tile_row0(const Tile &t, int i) {
+    return (i < t.sink ? i : i - t.sink + t.lo / kKeys) * kKeys;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
+    using C = PrefillCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *const sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *const kfull = reinterpret_cast<uint64_t *>(sm + C::OFF_BARS);
+    uint64_t *const kempty = kfull + 2, *const vfull = kempty + 2, *const vempty = vfull + 2;
+    uint64_t *const sfull = vempty + 2, *const pfull = sfull + 2, *const ofull = pfull + 2, *const qfull = ofull + 2;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(qfull + 1);
+    volatile int *const abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *const bad_page = abort + 1;
+    int *const sfound = const_cast<int *>(bad_page + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hk = a.c.kv_heads, h = blockIdx.x % hk;
+    const int slot_id = a.nslots - 1 - static_cast<int>(blockIdx.x / hk);  // the longest walks first
+
+    // ---- the sequence whose tiles hold this slot: tiles of sequence b start at slot floor(cu[b] G / 256) + b
+    if (tid == 0) *sfound = 0x7fffffff;
+    __syncthreads();
+    auto first_slot = [&](int b, int c) { return static_cast<long long>(c) * a.G / kRows + b; };
+    for (int b = tid; b < a.B; b += kPrefillThreads) {
+        const int c0 = a.cu[b], c1 = a.cu[b + 1];
+        if (first_slot(b, c0) <= slot_id && slot_id < first_slot(b + 1, c1)) atomicMin(sfound, b);
+        if (blockIdx.x == 0) {  // one CTA looks every sequence over
+            const int s = a.slots ? a.slots[b] : b;
+            bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.total && c1 - c0 <= a.max_rows && s >= 0 && s < a.c.max_seqs;
+            if (ok) ok = a.c.len[s] >= 0 && a.c.len[s] <= a.c.max_pages * a.c.page_size;
+            if (!ok) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+        }
+    }
+    __syncthreads();
+    Tile t;
+    t.b = *sfound;
+    if (t.b >= a.B) return;
+    t.c0 = a.cu[t.b];
+    const int c1 = a.cu[t.b + 1];
+    t.n = c1 - t.c0;
+    t.slot = a.slots ? a.slots[t.b] : t.b;
+    if (t.c0 < 0 || c1 < t.c0 || c1 > a.total || t.n > a.max_rows || t.slot < 0 || t.slot >= a.c.max_seqs) return;
+    t.len = a.c.len[t.slot];
+    if (t.len < 0 || t.len > a.c.max_pages * a.c.page_size) return;
+    const long long r0 = (slot_id - first_slot(t.b, t.c0)) * kRows, all_rows = static_cast<long long>(t.n) * a.G;
+    if (r0 < 0 || r0 >= all_rows) return;
+    t.r0 = static_cast<int>(r0);
+    const int rows = static_cast<int>(min(static_cast<long long>(kRows), all_rows - r0));
+    const int base = t.len - t.n;  // position of the sequence's first query token
+    const int p_lo = base + t.r0 / a.G;
+    int p_hi[2];  // last position of each half
+    p_hi[0] = base + (t.r0 + min(rows, 128) - 1) / a.G;
+    p_hi[1] = base + (t.r0 + rows - 1) / a.G;
+    t.lo = a.window ? max(0, p_lo - a.window + 1) : 0;
+    t.hi = p_hi[1] + 1;
+    t.sink = t.lo > 0 ? min((min(a.sinks, t.lo) + kKeys - 1) / kKeys, t.lo / kKeys) : 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[row * D + lane + 32 * e] = f32_to_bf16(l == 0.f ? 0.f : o[e] / l);
-    if (lse && lane == 0) lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+    for (int x = 0; x < 2; ++x)
+        t.tiles[x] = (x && rows <= 128) || p_hi[x] < 0 ? 0 : t.sink + p_hi[x] / kKeys + 1 - t.lo / kKeys;
+    const int ntiles = max(t.tiles[0], t.tiles[1]);
+
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&kfull[s], 1);
+            mbar_init(&kempty[s], 1);
+            mbar_init(&vfull[s], 1);
+            mbar_init(&vempty[s], 1);
+            mbar_init(&sfull[s], 1);
+            mbar_init(&pfull[s], 4);
+            mbar_init(&ofull[s], 1);
+        }
+        mbar_init(qfull, 8);
+        *abort = 0;
+        *bad_page = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      if (warp == 8) {
+        // ---- TMA: lane l brings box l of a tile (page l / (D / 64), 64-channel half l % (D / 64))
+        constexpr int HALVES = D / 64;
+        const int box_rows = min(a.c.page_size, kKeys), boxes = kKeys / box_rows * HALVES;
+        const int sub = lane / HALVES, half = lane % HALVES;
+        const int *const table = a.c.table + static_cast<size_t>(t.slot) * a.c.max_pages;
+        auto entry_of = [&](int i, bool &need) {
+            const int j = tile_row0(t, i) + sub * box_rows, je = min(j + box_rows, t.hi);
+            need = i < ntiles && lane < boxes && j < t.hi && (je > t.lo || j < a.sinks);
+            return need ? __ldg(table + (j >> a.c.page_shift)) : 0;
+        };
+        bool need;
+        int entry = entry_of(0, need), issued = 0;
+        for (int i = 0; i < ntiles; ++i) {
+            const int s = i & 1;
+            const uint32_t ph = (i >> 1) & 1;
+            const int j = tile_row0(t, i) + sub * box_rows;
+            bool use = need;
+            if (need && (entry < 0 || entry >= a.c.num_pages)) use = false, *bad_page = 1;
+            const int y = use ? (entry * hk + h) * a.c.page_size + (j & (a.c.page_size - 1)) : 0;
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, use)) * box_rows * 128u;
+            entry = entry_of(i + 1, need);  // in flight while this tile's stages come free
+            const uint32_t off = half * (kKeys * 128) + sub * box_rows * 128;
+            if (!wait_or_abort(&kempty[s], ph ^ 1, abort, a.status)) break;
+            if (lane == 0) mbar_expect_tx(&kfull[s], bytes);
+            __syncwarp();
+            if (use) tma_load_2d(sm + C::OFF_K + s * C::TILE + off, &a.tk, 64 * half, y, &kfull[s]);
+            if (!wait_or_abort(&vempty[s], ph ^ 1, abort, a.status)) break;
+            if (lane == 0) mbar_expect_tx(&vfull[s], bytes);
+            __syncwarp();
+            if (use) tma_load_2d(sm + C::OFF_V + s * C::TILE + off, &a.tv, 64 * half, y, &vfull[s]);
+            issued = i + 1;
+        }
+        if (*abort) {  // nobody consumes what is in flight any more: let it land before the CTA ends
+            for (int i = max(0, issued - 2); i < min(issued + 1, ntiles); ++i) {
+                mbar_wait(&kfull[i & 1], (i >> 1) & 1, 100000000LL);
+                if (i < issued) mbar_wait(&vfull[i & 1], (i >> 1) & 1, 100000000LL);
+            }
+        }
+      } else if (warp == 9) {
+        // ---- MMA
+        constexpr uint32_t id_s = idesc_bf16(128, kKeys, false, false), id_o = idesc_bf16(128, D, false, true);
+        const uint32_t sq = smem_u32(sm);
+        bool ok = ntiles > 0 && wait_or_abort(qfull, 0, abort, a.status);
+        auto scores = [&](int x, int i) {  // S_x = Q_x K_i^T
+            if (lane == 0) {
+                const uint64_t dq = kmaj_desc(sq + x * C::TILE, 128, 0, 0);
+                const uint64_t dk = kmaj_desc(sq + C::OFF_K + (i & 1) * C::TILE, kKeys, 0, 0);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16(tmem + 128 * x, dq + kmaj_step(128, ks), dk + kmaj_step(kKeys, ks), id_s, ks > 0);
+                mma_commit(&sfull[x]);
+            }
+        };
+        if (ok) ok = wait_or_abort(&kfull[0], 0, abort, a.status);
+        if (ok) {
+            tc_fence_after();
+            for (int x = 0; x < 2; ++x)
+                if (t.tiles[x] > 0) scores(x, 0);
+            if (lane == 0) mma_commit(&kempty[0]);
+        }
+        for (int i = 0; ok && i < ntiles; ++i) {
+            const int s = i & 1;
+            const uint32_t ph = (i >> 1) & 1;
+            uint8_t *const sv = sm + C::OFF_V + s * C::TILE;
+            if (!(ok = wait_or_abort(&vfull[s], ph, abort, a.status))) break;
+            // V rows that no row of this CTA sees: zeros
+            const int j0 = tile_row0(t, i);
+            const int z0 = max(j0, a.sinks) - j0, z1 = min(t.lo, j0 + kKeys) - j0, z2 = max(j0, t.hi) - j0;
+            if (z0 < z1 || z2 < kKeys) {
+                for (int e = lane; e < kKeys * (D / 8); e += 32) {
+                    const int r = e / (D / 8), c = e % (D / 8);
+                    if ((r >= z0 && r < z1) || r >= z2)
+                        *reinterpret_cast<uint4 *>(sv + kmaj_off(r, 8 * c, kKeys)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_async_smem();
+                __syncwarp();
+            }
+            bool next_k = false;
+            for (int x = 0; x < 2 && ok; ++x) {
+                if (i >= t.tiles[x]) continue;
+                if (!(ok = wait_or_abort(&pfull[x], i & 1, abort, a.status))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t dv = mnmaj_desc(smem_u32(sv), kKeys, 0, 0);
+#pragma unroll
+                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                        mma_bf16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 8 * ks, dv + mnmaj_step(ks), id_o, i > 0 || ks > 0);
+                    if (i + 1 == t.tiles[x]) mma_commit(&ofull[x]);
+                }
+                if (i + 1 < t.tiles[x]) {
+                    if (!next_k) {
+                        if (!(ok = wait_or_abort(&kfull[(i + 1) & 1], ((i + 1) >> 1) & 1, abort, a.status))) break;
+                        tc_fence_after();
+                        next_k = true;
+                    }
+                    scores(x, i + 1);
+                }
+            }
+            if (ok && lane == 0) {
+                mma_commit(&vempty[s]);
+                if (next_k) mma_commit(&kempty[(i + 1) & 1]);
+            }
+        }
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ---- softmax: this thread's row of half x
+        const int x = warp >> 2, r = 128 * x + 32 * (warp & 3) + lane;
+        const bool real = r < rows;
+        const int tok = (t.r0 + r) / a.G, g = t.r0 + r - tok * a.G;
+        const size_t row = static_cast<size_t>(t.c0 + (real ? tok : 0)) * a.heads + static_cast<size_t>(h) * a.G + (real ? g : 0);
+        const int pos = base + min(tok, t.n - 1);
+        {
+            const uint4 *const src = reinterpret_cast<const uint4 *>(a.q + row * D);
+            uint8_t *const dst = sm + x * C::TILE;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 v = real ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                v.x ^= a.flip;
+                v.y ^= a.flip;
+                v.z ^= a.flip;
+                v.w ^= a.flip;
+                *reinterpret_cast<uint4 *>(dst + kmaj_off(r & 127, 8 * c, 128)) = v;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull);
+        }
+        const uint32_t ts = tmem_lane_base(tmem, warp) + 128 * x, to = tmem_lane_base(tmem, warp) + 256 + 128 * x;
+        const int p_first = base + (t.r0 + 128 * x) / a.G, p_last = p_hi[x];
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int i = 0; i < t.tiles[x]; ++i) {
+            if (!(ok = wait_or_abort(&sfull[x], i & 1, abort, a.status))) break;
+            tc_fence_after();
+            float s[kKeys];
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 32) tmem_ld32(ts + c, s + c);
+            tmem_ld_wait();
+            const int j0 = tile_row0(t, i);
+            if (j0 + kKeys - 1 > p_first || (a.window && j0 <= p_last - a.window)) {
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) {
+                    const int j = j0 + c;
+                    const bool seen = j <= pos && (!a.window || j > pos - a.window || j < a.sinks);
+                    s[c] = seen ? s[c] : -INFINITY;
+                }
+            }
+            float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < kKeys; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
+            const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale2;
+            float f = 1.f;
+            if (mn > m + kGrow || m == -INFINITY) {  // -inf: the first rows this one sees; its O is still zero
+                const float mx = fmaxf(m, mn);
+                f = m == -INFINITY ? 0.f : ex2(m - mx);
+                m = mx;
+            }
+            if (i > 0 && __any_sync(0xffffffffu, f != 1.f && l != 0.f)) {
+#pragma unroll
+                for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    tmem_ld16(to + c, o);
+                    tmem_ld_wait();
+                    uint32_t u[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
+                    tmem_st16(to + c, u);
+                }
+            }
+            l *= f;
+            const float ref = m == -INFINITY ? 0.f : m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 32) {
+                uint32_t u[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float p0 = ex2(fmaf(s[c + 2 * e], a.scale2, -ref)), p1 = ex2(fmaf(s[c + 2 * e + 1], a.scale2, -ref));
+                    sum[e & 3] += p0 + p1;
+                    u[e] = pack_bf16(p0, p1);
+                }
+                tmem_st16(ts + c / 2, u);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[x]);
+        }
+        if (ok && t.tiles[x] > 0) ok = wait_or_abort(&ofull[x], 0, abort, a.status);
+        tc_fence_after();
+        if (ok && !*bad_page) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint4 *const dst = reinterpret_cast<uint4 *>(a.out + row * D);
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(to + c, o);
+                tmem_ld_wait();
+                if (t.tiles[x] == 0 || l == 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+                }
+                uint32_t u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+                if (real) {
+                    dst[c / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+                    dst[c / 8 + 1] = make_uint4(u[4], u[5], u[6], u[7]);
+                }
+            }
+            if (a.lse && real) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        } else if (*bad_page && tid == 0) {
+            atomicExch(a.status, KDA_ERR_INVALID_ARG);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// 2-D map over a layer's pool as rows of D values; boxes of 64 channels x min(page, 128) rows.
+int make_pool_map(CUtensorMap *tm, const void *base, const KvView &c, int D) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return KDA_ERR_CUDA;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(c.num_pages) * c.kv_heads * c.page_size};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(std::min(c.page_size, kKeys))};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KDA_OK : KDA_ERR_INVALID_ARG;
+}
+
+template <int D>
+int launch_prefill(const PrefillArgs &a, unsigned grid, cudaStream_t s) {
+    static std::atomic<unsigned long long> attr{0};
+    KDA_TRY(smem_opt_in(prefill_kernel<D>, PrefillCfg<D>::BYTES, attr));
+    prefill_kernel<D><<<grid, kPrefillThreads, PrefillCfg<D>::BYTES, s>>>(a);
+    return launch_status();
 }
 
 }  // namespace
@@ -69,16 +483,32 @@ extern "C" int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_
     if (B > 65535 || dims->heads > 65535) return KDA_ERR_UNSUPPORTED;
     if (B == 0 || total_tokens == 0) return KDA_OK;
     if (max_rows == 0) return KDA_ERR_INVALID_ARG;
-    int *status = kda::device_status_ptr();
-    if (!status) return KDA_ERR_CUDA;
-    const dim3 grid((max_rows + 3) / 4, dims->heads, B);
+    kda::PrefillArgs a{};
+    a.G = dims->heads / cache->kv_heads;
+    const long long slots_n = static_cast<long long>(total_tokens) * a.G / kda::kRows + B;
+    if (static_cast<long long>(total_tokens) * a.G > 0x7fffffffLL - kda::kRows || slots_n * cache->kv_heads > 0x7fffffffLL)
+        return KDA_ERR_UNSUPPORTED;
+    a.status = kda::device_status_ptr();
+    if (!a.status) return KDA_ERR_CUDA;
+    a.c = kda::kv_view(cache, layer);
+    KDA_TRY(kda::make_pool_map(&a.tk, a.c.k, a.c, cache->head_dim));
+    KDA_TRY(kda::make_pool_map(&a.tv, a.c.v, a.c, cache->head_dim));
+    a.q = q;
+    a.cu = cu_seqlens;
+    a.slots = slots;
+    a.out = out;
+    a.lse = lse;
+    a.B = B;
+    a.max_rows = max_rows;
+    a.total = total_tokens;
+    a.heads = dims->heads;
+    a.window = window;
+    a.sinks = sinks;
+    a.nslots = static_cast<int>(slots_n);
+    // a negative scale is taken as negated queries, and 0 as one so small that every weight is 1
+    a.scale2 = std::max(std::fabs(dims->scale) * 1.4426950408889634f, 1e-30f);
+    a.flip = dims->scale < 0.f ? 0x80008000u : 0u;
+    const unsigned grid = static_cast<unsigned>(slots_n * cache->kv_heads);
     auto s = static_cast<cudaStream_t>(stream);
-    const kda::KvView view = kda::kv_view(cache, layer);
-    if (dims->head_dim == 128)
-        kda::prefill_kernel<128><<<grid, 128, 0, s>>>(view, q, cu_seqlens, slots, B, max_rows, total_tokens, dims->heads,
-                                                     window, sinks, dims->scale, out, lse, status);
-    else
-        kda::prefill_kernel<64><<<grid, 128, 0, s>>>(view, q, cu_seqlens, slots, B, max_rows, total_tokens, dims->heads,
-                                                    window, sinks, dims->scale, out, lse, status);
-    return kda::launch_status();
+    return cache->head_dim == 128 ? kda::launch_prefill<128>(a, grid, s) : kda::launch_prefill<64>(a, grid, s);
 }
