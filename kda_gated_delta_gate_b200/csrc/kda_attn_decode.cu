@@ -553,8 +553,9 @@ int kda_attn_decode(const kda_kv_cache *cache, int layer, const kda_bf16 *q, con
     a.K = K;
     a.G = dims->heads / cache->kv_heads;
     a.heads = dims->heads;
-    a.window = window;
-    a.sinks = sinks;
+    // a window that holds the longest sequence is none
+    a.window = window < a.c.max_pages * a.c.page_size ? window : 0;
+    a.sinks = std::min(sinks, a.c.max_pages * a.c.page_size);
     a.scale2 = dims->scale * kda::kLog2e;
     const int rows = a.G * K, mt = kda::m_tiles(rows), D = dims->head_dim;
     const int grid = kda::ctas_per_sm(D, mt) * kda::num_sms();

@@ -14,7 +14,9 @@
 //   warp 8            TMA: K and V tiles page by page (one box of 64 channels per page, at most 128 rows),
 //                     128-byte swizzle, two stages each
 //   warp 9            tcgen05.mma: S_a, S_b; then per cache tile P_a V, next S_a, P_b V, next S_b, so that one half's
-//                     products run under the other half's softmax; P is the A operand from TMEM
+//                     products run under the other half's softmax; P is the A operand from TMEM, taken in two
+//                     halves of 64 keys as the softmax finishes them
+//   warp 10           zeros in the V rows of edge tiles that no row of the CTA sees
 // O is rescaled only when a row's maximum has grown by more than 2^8 since its reference was set (P then
 // stays below 2^8, harmless in BF16 and FP32); a commit of S_x(i) also covers P_x(i - 1) V, so O needs no barrier of its own.
 // TMEM columns: S_a 0, S_b 128, O_a 256, O_b 384. P is rounded to BF16 for the second product (half a
@@ -111,11 +113,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+// One try with the hardware's own suspend time: the waits here are short and on the critical chain (2 % faster than
+// the long hint of mbar_try_wait, 8192 rows x 32 heads).
+__device__ __forceinline__ uint32_t try_wait(uint32_t addr, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    return done;
+}
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
     const uint32_t addr = smem_u32(bar);
-    if (mbar_try_wait(addr, parity)) return true;
+    if (try_wait(addr, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try_wait(addr, parity)) {
+    while (!try_wait(addr, parity)) {
         if (*abort) return false;
         if (clock64() - t0 > kPrefillWait) {
             *abort = 1;
@@ -125,6 +140,35 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
     }
     return true;
 }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two FP32 values in one 64-bit register: the paired multiply-add and add issue once for both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The n lowest bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t ones_below(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); }
 
 // Where a CTA's rows stand: the sequence's length and rows, and per half the positions and cache tiles.
 struct Tile {
@@ -137,6 +181,12 @@ __device__ __forceinline__ int tile_row0(const Tile &t, int i) {
     return (i < t.sink ? i : i - t.sink + t.lo / kKeys) * kKeys;
 }
 
+// Whether cache tile i has rows that no row of the CTA sees.
+__device__ __forceinline__ bool has_dead_rows(const Tile &t, int i, int sinks) {
+    const int j0 = tile_row0(t, i);
+    return j0 + kKeys > t.hi || max(j0, sinks) < min(t.lo, j0 + kKeys);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
     using C = PrefillCfg<D>;
@@ -144,7 +194,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     uint8_t *const sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *const kfull = reinterpret_cast<uint64_t *>(sm + C::OFF_BARS);
     uint64_t *const kempty = kfull + 2, *const vfull = kempty + 2, *const vempty = vfull + 2;
-    uint64_t *const sfull = vempty + 2, *const pfull = sfull + 2, *const ofull = pfull + 2, *const qfull = ofull + 2;
+    uint64_t *const sfull = vempty + 2, *const pfull = sfull + 2, *const ofull = pfull + 4, *const vfix = ofull + 2;
+    uint64_t *const fixgo = vfix + 2, *const qfull = fixgo + 2;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(qfull + 1);
     volatile int *const abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *const bad_page = abort + 1;
@@ -188,7 +239,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     int p_hi[2];  // last position of each half
     p_hi[0] = base + (t.r0 + min(rows, 128) - 1) / a.G;
     p_hi[1] = base + (t.r0 + rows - 1) / a.G;
-    t.lo = a.window ? max(0, p_lo - a.window + 1) : 0;
+    t.lo = a.window ? static_cast<int>(max(0LL, static_cast<long long>(p_lo) - a.window + 1)) : 0;
     t.hi = p_hi[1] + 1;
     t.sink = t.lo > 0 ? min((min(a.sinks, t.lo) + kKeys - 1) / kKeys, t.lo / kKeys) : 0;
 #pragma unroll
@@ -204,6 +255,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             mbar_init(&vempty[s], 1);
             mbar_init(&sfull[s], 1);
             mbar_init(&pfull[s], 4);
+            mbar_init(&pfull[2 + s], 4);
+            mbar_init(&vfix[s], 1);
+            mbar_init(&fixgo[s], 1);
             mbar_init(&ofull[s], 1);
         }
         mbar_init(qfull, 8);
@@ -253,6 +307,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             if (lane == 0) mbar_expect_tx(&vfull[s], bytes);
             __syncwarp();
             if (use) tma_load_2d(sm + C::OFF_V + s * C::TILE + off, &a.tv, 64 * half, y, &vfull[s]);
+            if (lane == 0 && has_dead_rows(t, i, a.sinks)) mbar_arrive(&fixgo[s]);
             issued = i + 1;
         }
         if (*abort) {  // nobody consumes what is in flight any more: let it land before the CTA ends
@@ -262,69 +317,76 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             }
         }
       } else if (warp == 9) {
-        // ---- MMA
-        constexpr uint32_t id_s = idesc_bf16(128, kKeys, false, false), id_o = idesc_bf16(128, D, false, true);
-        const uint32_t sq = smem_u32(sm);
-        bool ok = ntiles > 0 && wait_or_abort(qfull, 0, abort, a.status);
-        auto scores = [&](int x, int i) {  // S_x = Q_x K_i^T
-            if (lane == 0) {
+        // ---- MMA, one thread; what it waits for is nearly always there but P
+        if (lane == 0 && ntiles > 0) {
+            constexpr uint32_t id_s = idesc_bf16(128, kKeys, false, false), id_o = idesc_bf16(128, D, false, true);
+            const uint32_t sq = smem_u32(sm);
+            uint32_t fixes = 0;  // bit s: parity of the next zeroed V tile in stage s
+            auto scores = [&](int x, int i) {  // S_x = Q_x K_i^T
                 const uint64_t dq = kmaj_desc(sq + x * C::TILE, 128, 0, 0);
                 const uint64_t dk = kmaj_desc(sq + C::OFF_K + (i & 1) * C::TILE, kKeys, 0, 0);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     mma_bf16(tmem + 128 * x, dq + kmaj_step(128, ks), dk + kmaj_step(kKeys, ks), id_s, ks > 0);
                 mma_commit(&sfull[x]);
-            }
-        };
-        if (ok) ok = wait_or_abort(&kfull[0], 0, abort, a.status);
-        if (ok) {
-            tc_fence_after();
-            for (int x = 0; x < 2; ++x)
-                if (t.tiles[x] > 0) scores(x, 0);
-            if (lane == 0) mma_commit(&kempty[0]);
-        }
-        for (int i = 0; ok && i < ntiles; ++i) {
-            const int s = i & 1;
-            const uint32_t ph = (i >> 1) & 1;
-            uint8_t *const sv = sm + C::OFF_V + s * C::TILE;
-            if (!(ok = wait_or_abort(&vfull[s], ph, abort, a.status))) break;
-            // V rows that no row of this CTA sees: zeros
-            const int j0 = tile_row0(t, i);
-            const int z0 = max(j0, a.sinks) - j0, z1 = min(t.lo, j0 + kKeys) - j0, z2 = max(j0, t.hi) - j0;
-            if (z0 < z1 || z2 < kKeys) {
-                for (int e = lane; e < kKeys * (D / 8); e += 32) {
-                    const int r = e / (D / 8), c = e % (D / 8);
-                    if ((r >= z0 && r < z1) || r >= z2)
-                        *reinterpret_cast<uint4 *>(sv + kmaj_off(r, 8 * c, kKeys)) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_async_smem();
-                __syncwarp();
-            }
-            bool next_k = false;
-            for (int x = 0; x < 2 && ok; ++x) {
-                if (i >= t.tiles[x]) continue;
-                if (!(ok = wait_or_abort(&pfull[x], i & 1, abort, a.status))) break;
+            };
+            bool ok = wait_or_abort(qfull, 0, abort, a.status) && wait_or_abort(&kfull[0], 0, abort, a.status);
+            if (ok) {
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t dv = mnmaj_desc(smem_u32(sv), kKeys, 0, 0);
+                for (int x = 0; x < 2; ++x)
+                    if (t.tiles[x] > 0) scores(x, 0);
+                mma_commit(&kempty[0]);
+            }
+            for (int i = 0; ok && i < ntiles; ++i) {
+                const int s = i & 1;
+                ok = wait_or_abort(&vfull[s], (i >> 1) & 1, abort, a.status);
+                if (ok && has_dead_rows(t, i, a.sinks)) {
+                    ok = wait_or_abort(&vfix[s], (fixes >> s) & 1, abort, a.status);
+                    fixes ^= 1u << s;
+                }
+                if (ok && i + 1 < ntiles) ok = wait_or_abort(&kfull[s ^ 1], ((i + 1) >> 1) & 1, abort, a.status);
+                const uint64_t dv = mnmaj_desc(sq + C::OFF_V + s * C::TILE, kKeys, 0, 0);
 #pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)
-                        mma_bf16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 8 * ks, dv + mnmaj_step(ks), id_o, i > 0 || ks > 0);
-                    if (i + 1 == t.tiles[x]) mma_commit(&ofull[x]);
-                }
-                if (i + 1 < t.tiles[x]) {
-                    if (!next_k) {
-                        if (!(ok = wait_or_abort(&kfull[(i + 1) & 1], ((i + 1) >> 1) & 1, abort, a.status))) break;
-                        tc_fence_after();
-                        next_k = true;
+                for (int x = 0; x < 2; ++x) {
+                    if (ok && i < t.tiles[x]) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {  // P comes in two halves of 64 keys
+                            if (ok) ok = wait_or_abort(&pfull[2 * half + x], i & 1, abort, a.status);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                                mma_bf16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 8 * ks, dv + mnmaj_step(ks), id_o, i > 0 || ks > 0);
+                        }
+                        if (ok && i + 1 < t.tiles[x]) scores(x, i + 1);
+                        else if (ok) mma_commit(&ofull[x]);
                     }
-                    scores(x, i + 1);
+                }
+                if (ok) {
+                    mma_commit(&vempty[s]);
+                    if (i + 1 < ntiles) mma_commit(&kempty[s ^ 1]);
                 }
             }
-            if (ok && lane == 0) {
-                mma_commit(&vempty[s]);
-                if (next_k) mma_commit(&kempty[(i + 1) & 1]);
+        }
+      } else if (warp == 10) {
+        // ---- V rows that no row of this CTA sees: zeros. fixgo says that the tile's load is under way, so that
+        // vfull's phase is the tile's own (tiles without such rows pass unseen here)
+        uint32_t gone = 0;
+        for (int i = 0; i < ntiles; ++i) {
+            if (!has_dead_rows(t, i, a.sinks)) continue;
+            uint8_t *const sv = sm + C::OFF_V + (i & 1) * C::TILE;
+            if (!wait_or_abort(&fixgo[i & 1], (gone >> (i & 1)) & 1, abort, a.status)) break;
+            gone ^= 1u << (i & 1);
+            if (!wait_or_abort(&vfull[i & 1], (i >> 1) & 1, abort, a.status)) break;
+            const int j0 = tile_row0(t, i);
+            for (int e = lane; e < kKeys * (D / 8); e += 32) {
+                const int r = e / (D / 8), c = e % (D / 8), j = j0 + r;
+                if (j >= t.hi || (j < t.lo && j >= a.sinks))
+                    *reinterpret_cast<uint4 *>(sv + kmaj_off(r, 8 * c, kKeys)) = make_uint4(0u, 0u, 0u, 0u);
             }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vfix[i & 1]);
         }
       }
     } else {
@@ -364,17 +426,24 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             tmem_ld_wait();
             const int j0 = tile_row0(t, i);
             if (j0 + kKeys - 1 > p_first || (a.window && j0 <= p_last - a.window)) {
+                // one bit per column: [first, pos] and the sinks, as shifts of ones
+                const int last = pos - j0, first = a.window ? last - a.window + 1 : -j0, sink = a.sinks - j0;
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c) {
-                    const int j = j0 + c;
-                    const bool seen = j <= pos && (!a.window || j > pos - a.window || j < a.sinks);
-                    s[c] = seen ? s[c] : -INFINITY;
+                for (int c = 0; c < kKeys; c += 32) {
+                    const uint32_t to_pos = ones_below(last + 1 - c);
+                    const uint32_t seen = to_pos & (~ones_below(first - c) | ones_below(sink - c));
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) s[c + e] = seen & (1u << e) ? s[c + e] : -INFINITY;
                 }
             }
             float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int c = 4; c < kKeys; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
-            const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale2;
+            for (int c = 4; c < kKeys - 4; c += 8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top[e] = max3(top[e], s[c + e], s[c + 4 + e]);
+            }
+            const float mn = max3(max3(top[0], s[kKeys - 4], s[kKeys - 3]), max3(top[1], s[kKeys - 2], s[kKeys - 1]),
+                                  fmaxf(top[2], top[3])) * a.scale2;
             float f = 1.f;
             if (mn > m + kGrow || m == -INFINITY) {  // -inf: the first rows this one sees; its O is still zero
                 const float mx = fmaxf(m, mn);
@@ -395,23 +464,31 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             }
             l *= f;
             const float ref = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t scale_2 = pair(a.scale2, a.scale2), ref_2 = pair(-ref, -ref);
+            uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < kKeys; c += 32) {
                 uint32_t u[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float p0 = ex2(fmaf(s[c + 2 * e], a.scale2, -ref)), p1 = ex2(fmaf(s[c + 2 * e + 1], a.scale2, -ref));
-                    sum[e & 3] += p0 + p1;
+                    float p0, p1;
+                    unpair(fma2(pair(s[c + 2 * e], s[c + 2 * e + 1]), scale_2, ref_2), p0, p1);
+                    p0 = ex2(p0);
+                    p1 = ex2(p1);
+                    sum[e & 1] = add2(sum[e & 1], pair(p0, p1));
                     u[e] = pack_bf16(p0, p1);
                 }
                 tmem_st16(ts + c / 2, u);
+                if (c == 32 || c == 96) {  // 64 keys' weights are there: their half of the product may start
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[(c == 96 ? 2 : 0) + x]);
+                }
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[x]);
+            float sum_lo, sum_hi;
+            unpair(add2(sum[0], sum[1]), sum_lo, sum_hi);
+            l += sum_lo + sum_hi;
         }
         if (ok && t.tiles[x] > 0) ok = wait_or_abort(&ofull[x], 0, abort, a.status);
         tc_fence_after();
@@ -502,8 +579,9 @@ extern "C" int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_
     a.max_rows = max_rows;
     a.total = total_tokens;
     a.heads = dims->heads;
-    a.window = window;
-    a.sinks = sinks;
+    // a window that holds the longest sequence is none
+    a.window = window < a.c.max_pages * a.c.page_size ? window : 0;
+    a.sinks = std::min(sinks, a.c.max_pages * a.c.page_size);
     a.nslots = static_cast<int>(slots_n);
     // a negative scale is taken as negated queries, and 0 as one so small that every weight is 1
     a.scale2 = std::max(std::fabs(dims->scale) * 1.4426950408889634f, 1e-30f);
