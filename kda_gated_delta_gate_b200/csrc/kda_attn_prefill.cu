@@ -167,6 +167,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// True in one lane of a converged warp. The MMA role runs with its whole warp and branches on this around the
+// instructions that one thread issues: their operands then stay warp-uniform.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
+}
+
 // The n lowest bits (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t ones_below(int n) { return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u); }
 
@@ -175,7 +187,7 @@ struct Tile {
     int b, slot, c0, n, len, r0;  // r0: first of the 256 rows (token * G + head)
     int lo, hi;                   // visible cached rows: [lo, hi) and those below `sinks`
     int sink;                     // leading tiles that only sinks need
-    int tiles[2];                 // per half
+    int tiles_a, tiles_b;         // per half
 };
 __device__ __forceinline__ int tile_row0(const Tile &t, int i) {
     return (i < t.sink ? i : i - t.sink + t.lo / kKeys) * kKeys;
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     volatile int *const bad_page = abort + 1;
     int *const sfound = const_cast<int *>(bad_page + 1);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int hk = a.c.kv_heads, h = blockIdx.x % hk;
     const int slot_id = a.nslots - 1 - static_cast<int>(blockIdx.x / hk);  // the longest walks first
 
@@ -236,16 +248,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     const int rows = static_cast<int>(min(static_cast<long long>(kRows), all_rows - r0));
     const int base = t.len - t.n;  // position of the sequence's first query token
     const int p_lo = base + t.r0 / a.G;
-    int p_hi[2];  // last position of each half
-    p_hi[0] = base + (t.r0 + min(rows, 128) - 1) / a.G;
-    p_hi[1] = base + (t.r0 + rows - 1) / a.G;
+    const int p_hi_a = base + (t.r0 + min(rows, 128) - 1) / a.G, p_hi_b = base + (t.r0 + rows - 1) / a.G;  // last positions
     t.lo = a.window ? static_cast<int>(max(0LL, static_cast<long long>(p_lo) - a.window + 1)) : 0;
-    t.hi = p_hi[1] + 1;
+    t.hi = p_hi_b + 1;
     t.sink = t.lo > 0 ? min((min(a.sinks, t.lo) + kKeys - 1) / kKeys, t.lo / kKeys) : 0;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-        t.tiles[x] = (x && rows <= 128) || p_hi[x] < 0 ? 0 : t.sink + p_hi[x] / kKeys + 1 - t.lo / kKeys;
-    const int ntiles = max(t.tiles[0], t.tiles[1]);
+    t.tiles_a = p_hi_a < 0 ? 0 : t.sink + p_hi_a / kKeys + 1 - t.lo / kKeys;
+    t.tiles_b = rows <= 128 || p_hi_b < 0 ? 0 : t.sink + p_hi_b / kKeys + 1 - t.lo / kKeys;
+    const int ntiles = max(t.tiles_a, t.tiles_b);
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -272,7 +281,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp >= 8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -317,54 +326,75 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             }
         }
       } else if (warp == 9) {
-        // ---- MMA, one thread; what it waits for is nearly always there but P
-        if (lane == 0 && ntiles > 0) {
+        // ---- MMA; what it waits for is nearly always there but P
+        if (ntiles > 0) {
             constexpr uint32_t id_s = idesc_bf16(128, kKeys, false, false), id_o = idesc_bf16(128, D, false, true);
             const uint32_t sq = smem_u32(sm);
             uint32_t fixes = 0;  // bit s: parity of the next zeroed V tile in stage s
+            auto commit = [&](uint64_t *bar) {
+                if (elect_one()) mma_commit(bar);
+                __syncwarp();
+            };
             auto scores = [&](int x, int i) {  // S_x = Q_x K_i^T
                 const uint64_t dq = kmaj_desc(sq + x * C::TILE, 128, 0, 0);
                 const uint64_t dk = kmaj_desc(sq + C::OFF_K + (i & 1) * C::TILE, kKeys, 0, 0);
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    mma_bf16(tmem + 128 * x, dq + kmaj_step(128, ks), dk + kmaj_step(kKeys, ks), id_s, ks > 0);
-                mma_commit(&sfull[x]);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_bf16(tmem + 128 * x, dq + kmaj_step(128, ks), dk + kmaj_step(kKeys, ks), id_s, ks > 0);
+                    mma_commit(&sfull[x]);
+                }
+                __syncwarp();
             };
-            bool ok = wait_or_abort(qfull, 0, abort, a.status) && wait_or_abort(&kfull[0], 0, abort, a.status);
-            if (ok) {
-                tc_fence_after();
-                for (int x = 0; x < 2; ++x)
-                    if (t.tiles[x] > 0) scores(x, 0);
-                mma_commit(&kempty[0]);
-            }
-            for (int i = 0; ok && i < ntiles; ++i) {
+            // tile i's V and tile i + 1's K
+            auto operands = [&](int i) {
                 const int s = i & 1;
-                ok = wait_or_abort(&vfull[s], (i >> 1) & 1, abort, a.status);
+                bool ok = wait_or_abort(&vfull[s], (i >> 1) & 1, abort, a.status);
                 if (ok && has_dead_rows(t, i, a.sinks)) {
                     ok = wait_or_abort(&vfix[s], (fixes >> s) & 1, abort, a.status);
                     fixes ^= 1u << s;
                 }
                 if (ok && i + 1 < ntiles) ok = wait_or_abort(&kfull[s ^ 1], ((i + 1) >> 1) & 1, abort, a.status);
+                return ok;
+            };
+            bool ok = wait_or_abort(qfull, 0, abort, a.status) && wait_or_abort(&kfull[0], 0, abort, a.status);
+            if (ok) {
+                tc_fence_after();
+                if (t.tiles_a > 0) scores(0, 0);
+                if (t.tiles_b > 0) scores(1, 0);
+                commit(&kempty[0]);
+                ok = operands(0);
+            }
+            for (int i = 0; ok && i < ntiles; ++i) {
+                const int s = i & 1;
                 const uint64_t dv = mnmaj_desc(sq + C::OFF_V + s * C::TILE, kKeys, 0, 0);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (ok && i < t.tiles[x]) {
+                    const int tiles = x ? t.tiles_b : t.tiles_a;
+                    if (ok && i < tiles) {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {  // P comes in two halves of 64 keys
                             if (ok) ok = wait_or_abort(&pfull[2 * half + x], i & 1, abort, a.status);
                             if (!ok) break;
                             tc_fence_after();
+                            if (elect_one()) {
 #pragma unroll
-                            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                                mma_bf16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 8 * ks, dv + mnmaj_step(ks), id_o, i > 0 || ks > 0);
+                                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                                    mma_bf16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 8 * ks, dv + mnmaj_step(ks), id_o, i > 0 || ks > 0);
+                            }
+                            __syncwarp();
                         }
-                        if (ok && i + 1 < t.tiles[x]) scores(x, i + 1);
-                        else if (ok) mma_commit(&ofull[x]);
+                        if (!ok) break;
+                        if (x == 1) commit(&vempty[s]);
+                        if (i + 1 < tiles) scores(x, i + 1);
+                        else commit(&ofull[x]);
+                    } else if (x == 1) {
+                        commit(&vempty[s]);
                     }
                 }
-                if (ok) {
-                    mma_commit(&vempty[s]);
-                    if (i + 1 < ntiles) mma_commit(&kempty[s ^ 1]);
+                if (ok && i + 1 < ntiles) {  // the next operands are looked for while S_b is still running
+                    commit(&kempty[s ^ 1]);
+                    ok = operands(i + 1);
                 }
             }
         }
@@ -414,10 +444,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             if (lane == 0) mbar_arrive(qfull);
         }
         const uint32_t ts = tmem_lane_base(tmem, warp) + 128 * x, to = tmem_lane_base(tmem, warp) + 256 + 128 * x;
-        const int p_first = base + (t.r0 + 128 * x) / a.G, p_last = p_hi[x];
+        const int p_first = base + (t.r0 + 128 * x) / a.G, p_last = x ? p_hi_b : p_hi_a, tiles = x ? t.tiles_b : t.tiles_a;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int i = 0; i < t.tiles[x]; ++i) {
+        for (int i = 0; i < tiles; ++i) {
             if (!(ok = wait_or_abort(&sfull[x], i & 1, abort, a.status))) break;
             tc_fence_after();
             float s[kKeys];
@@ -490,7 +520,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             unpair(add2(sum[0], sum[1]), sum_lo, sum_hi);
             l += sum_lo + sum_hi;
         }
-        if (ok && t.tiles[x] > 0) ok = wait_or_abort(&ofull[x], 0, abort, a.status);
+        if (ok && tiles > 0) ok = wait_or_abort(&ofull[x], 0, abort, a.status);
         tc_fence_after();
         if (ok && !*bad_page) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -500,7 +530,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
                 float o[16];
                 tmem_ld16(to + c, o);
                 tmem_ld_wait();
-                if (t.tiles[x] == 0 || l == 0.f) {
+                if (tiles == 0 || l == 0.f) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = 0.f;
                 }
