@@ -193,10 +193,10 @@ __device__ __forceinline__ int tile_row0(const Tile &t, int i) {
     return (i < t.sink ? i : i - t.sink + t.lo / kKeys) * kKeys;
 }
 
-// Whether cache tile i has rows that no row of the CTA sees.
-__device__ __forceinline__ bool has_dead_rows(const Tile &t, int i, int sinks) {
-    const int j0 = tile_row0(t, i);
-    return j0 + kKeys > t.hi || max(j0, sinks) < min(t.lo, j0 + kKeys);
+// Whether cache tile i may have rows that no row of the CTA sees: the last tile, and where a window has
+// passed the start, the sinks' tiles and the window's first.
+__device__ __forceinline__ bool has_dead_rows(const Tile &t, int i, int ntiles) {
+    return i + 1 == ntiles || (t.lo > 0 && i <= t.sink);
 }
 
 template <int D>
@@ -204,9 +204,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     using C = PrefillCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *const kfull = reinterpret_cast<uint64_t *>(sm + C::OFF_BARS);
-    uint64_t *const kempty = kfull + 2, *const vfull = kempty + 2, *const vempty = vfull + 2;
-    uint64_t *const sfull = vempty + 2, *const pfull = sfull + 2, *const ofull = pfull + 4, *const vfix = ofull + 2;
+    // full[s]: V of tile i and K of tile i + 1, i % 2 = s, have landed ; empty[s]: they are read; first_k and
+    // first_read: the same for K of tile 0
+    uint64_t *const full = reinterpret_cast<uint64_t *>(sm + C::OFF_BARS);
+    uint64_t *const empty = full + 2, *const first_k = empty + 2, *const first_read = first_k + 1;
+    uint64_t *const sfull = first_read + 1, *const pfull = sfull + 2, *const ofull = pfull + 4, *const vfix = ofull + 2;
     uint64_t *const fixgo = vfix + 2, *const qfull = fixgo + 2;
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(qfull + 1);
     volatile int *const abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -258,10 +260,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&kfull[s], 1);
-            mbar_init(&kempty[s], 1);
-            mbar_init(&vfull[s], 1);
-            mbar_init(&vempty[s], 1);
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
             mbar_init(&sfull[s], 1);
             mbar_init(&pfull[s], 4);
             mbar_init(&pfull[2 + s], 4);
@@ -270,6 +270,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             mbar_init(&ofull[s], 1);
         }
         mbar_init(qfull, 8);
+        mbar_init(first_k, 1);
+        mbar_init(first_read, 1);
         *abort = 0;
         *bad_page = 0;
         fence_mbar_init();
@@ -296,34 +298,47 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             need = i < ntiles && lane < boxes && j < t.hi && (je > t.lo || j < a.sinks);
             return need ? __ldg(table + (j >> a.c.page_shift)) : 0;
         };
-        bool need;
+        struct Box {
+            bool use;
+            int y;
+        };
+        // this lane's box of tile i, and what it adds to the barrier's bytes (all lanes call)
+        auto box_of = [&](int i, int entry, bool need) {
+            const int j = tile_row0(t, i) + sub * box_rows;
+            const bool page = entry >= 0 && entry < a.c.num_pages;
+            if (need && !page) *bad_page = 1;
+            return Box{need && page, page ? (entry * hk + h) * a.c.page_size + (j & (a.c.page_size - 1)) : 0};
+        };
+        auto bytes_of = [&](const Box &b) { return __popc(__ballot_sync(0xffffffffu, b.use)) * box_rows * 128u; };
+        const uint32_t off = half * (kKeys * 128) + sub * box_rows * 128;
+        bool need = false;
         int entry = entry_of(0, need), issued = 0;
+        Box now = box_of(0, entry, need);
+        if (ntiles > 0) {
+            const uint32_t bytes = bytes_of(now);
+            if (lane == 0) mbar_expect_tx(first_k, bytes);
+            __syncwarp();
+            if (now.use) tma_load_2d(sm + C::OFF_K + off, &a.tk, 64 * half, now.y, first_k);
+        }
+        entry = entry_of(1, need);
         for (int i = 0; i < ntiles; ++i) {
             const int s = i & 1;
-            const uint32_t ph = (i >> 1) & 1;
-            const int j = tile_row0(t, i) + sub * box_rows;
-            bool use = need;
-            if (need && (entry < 0 || entry >= a.c.num_pages)) use = false, *bad_page = 1;
-            const int y = use ? (entry * hk + h) * a.c.page_size + (j & (a.c.page_size - 1)) : 0;
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, use)) * box_rows * 128u;
-            entry = entry_of(i + 1, need);  // in flight while this tile's stages come free
-            const uint32_t off = half * (kKeys * 128) + sub * box_rows * 128;
-            if (!wait_or_abort(&kempty[s], ph ^ 1, abort, a.status)) break;
-            if (lane == 0) mbar_expect_tx(&kfull[s], bytes);
+            const Box next = box_of(i + 1, entry, need);
+            const uint32_t bytes = bytes_of(now) + bytes_of(next);
+            entry = entry_of(i + 2, need);  // in flight while this tile's stage comes free
+            if (!wait_or_abort(&empty[s], ((i >> 1) & 1) ^ 1, abort, a.status)) break;
+            if (i == 1 && !wait_or_abort(first_read, 0, abort, a.status)) break;  // K of tile 2 goes where K of tile 0 was
+            if (lane == 0) mbar_expect_tx(&full[s], bytes);
             __syncwarp();
-            if (use) tma_load_2d(sm + C::OFF_K + s * C::TILE + off, &a.tk, 64 * half, y, &kfull[s]);
-            if (!wait_or_abort(&vempty[s], ph ^ 1, abort, a.status)) break;
-            if (lane == 0) mbar_expect_tx(&vfull[s], bytes);
-            __syncwarp();
-            if (use) tma_load_2d(sm + C::OFF_V + s * C::TILE + off, &a.tv, 64 * half, y, &vfull[s]);
-            if (lane == 0 && has_dead_rows(t, i, a.sinks)) mbar_arrive(&fixgo[s]);
+            if (now.use) tma_load_2d(sm + C::OFF_V + s * C::TILE + off, &a.tv, 64 * half, now.y, &full[s]);
+            if (next.use) tma_load_2d(sm + C::OFF_K + (s ^ 1) * C::TILE + off, &a.tk, 64 * half, next.y, &full[s]);
+            if (lane == 0 && has_dead_rows(t, i, ntiles)) mbar_arrive(&fixgo[s]);
             issued = i + 1;
+            now = next;
         }
-        if (*abort) {  // nobody consumes what is in flight any more: let it land before the CTA ends
-            for (int i = max(0, issued - 2); i < min(issued + 1, ntiles); ++i) {
-                mbar_wait(&kfull[i & 1], (i >> 1) & 1, 100000000LL);
-                if (i < issued) mbar_wait(&vfull[i & 1], (i >> 1) & 1, 100000000LL);
-            }
+        if (*abort && ntiles > 0) {  // nobody consumes what is in flight any more: let it land before the CTA ends
+            mbar_wait(first_k, 0, 100000000LL);
+            for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(&full[i & 1], (i >> 1) & 1, 100000000LL);
         }
       } else if (warp == 9) {
         // ---- MMA; what it waits for is nearly always there but P
@@ -349,20 +364,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             // tile i's V and tile i + 1's K
             auto operands = [&](int i) {
                 const int s = i & 1;
-                bool ok = wait_or_abort(&vfull[s], (i >> 1) & 1, abort, a.status);
-                if (ok && has_dead_rows(t, i, a.sinks)) {
+                bool ok = wait_or_abort(&full[s], (i >> 1) & 1, abort, a.status);
+                if (ok && has_dead_rows(t, i, ntiles)) {
                     ok = wait_or_abort(&vfix[s], (fixes >> s) & 1, abort, a.status);
                     fixes ^= 1u << s;
                 }
-                if (ok && i + 1 < ntiles) ok = wait_or_abort(&kfull[s ^ 1], ((i + 1) >> 1) & 1, abort, a.status);
                 return ok;
             };
-            bool ok = wait_or_abort(qfull, 0, abort, a.status) && wait_or_abort(&kfull[0], 0, abort, a.status);
+            bool ok = wait_or_abort(qfull, 0, abort, a.status) && wait_or_abort(first_k, 0, abort, a.status);
             if (ok) {
                 tc_fence_after();
                 if (t.tiles_a > 0) scores(0, 0);
                 if (t.tiles_b > 0) scores(1, 0);
-                commit(&kempty[0]);
+                commit(first_read);
                 ok = operands(0);
             }
             for (int i = 0; ok && i < ntiles; ++i) {
@@ -385,29 +399,26 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
                             __syncwarp();
                         }
                         if (!ok) break;
-                        if (x == 1) commit(&vempty[s]);
                         if (i + 1 < tiles) scores(x, i + 1);
                         else commit(&ofull[x]);
-                    } else if (x == 1) {
-                        commit(&vempty[s]);
                     }
                 }
                 if (ok && i + 1 < ntiles) {  // the next operands are looked for while S_b is still running
-                    commit(&kempty[s ^ 1]);
+                    commit(&empty[s]);
                     ok = operands(i + 1);
                 }
             }
         }
       } else if (warp == 10) {
         // ---- V rows that no row of this CTA sees: zeros. fixgo says that the tile's load is under way, so that
-        // vfull's phase is the tile's own (tiles without such rows pass unseen here)
+        // full's phase is the tile's own (tiles without such rows pass unseen here)
         uint32_t gone = 0;
         for (int i = 0; i < ntiles; ++i) {
-            if (!has_dead_rows(t, i, a.sinks)) continue;
+            if (!has_dead_rows(t, i, ntiles)) continue;
             uint8_t *const sv = sm + C::OFF_V + (i & 1) * C::TILE;
             if (!wait_or_abort(&fixgo[i & 1], (gone >> (i & 1)) & 1, abort, a.status)) break;
             gone ^= 1u << (i & 1);
-            if (!wait_or_abort(&vfull[i & 1], (i >> 1) & 1, abort, a.status)) break;
+            if (!wait_or_abort(&full[i & 1], (i >> 1) & 1, abort, a.status)) break;
             const int j0 = tile_row0(t, i);
             for (int e = lane; e < kKeys * (D / 8); e += 32) {
                 const int r = e / (D / 8), c = e % (D / 8), j = j0 + r;
