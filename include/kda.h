@@ -743,6 +743,8 @@ KDA_API size_t kda_attn_decode_scratch_bytes(int N, int K, const kda_dims *dims,
  *   q, out      [total_tokens, heads, head_dim] BF16;  lse [total_tokens, heads] F32 or NULL
  *   cu_seqlens  DEVICE int32 [B + 1];  slots  DEVICE int32 [B] or NULL (slot i); a slot may be listed more than once
  *   max_rows    at least n_i for every sequence
+ *   scratch     at least kda_attn_prefill_scratch_bytes(B, max_rows, total_tokens, dims, cache) bytes, 16-byte aligned
+ *               (NULL where that is 0); contents on entry do not matter
  *   other arguments as kda_attn_decode
  * Rows at or past cu_seqlens[B] are left as they were. A sequence with bad bounds (negative, decreasing,
  * past total_tokens, or longer than max_rows; where cu_seqlens decreases, its other sequences
@@ -752,7 +754,13 @@ KDA_API size_t kda_attn_decode_scratch_bytes(int N, int K, const kda_dims *dims,
  * window of all rows of a query tile, has no effect; V rows that a row of the call sees must be finite. */
 KDA_API int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *cu_seqlens,
                              const int *slots, int B, int max_rows, int total_tokens, int window, int sinks,
-                             kda_bf16 *out, float *lse, const kda_dims *dims, void *stream);
+                             kda_bf16 *out, float *lse, void *scratch, size_t scratch_bytes, const kda_dims *dims,
+                             void *stream);
+
+/* Scratch bytes of kda_attn_prefill on the current device: 0 where its rows fill the SMs (or a size is 0 or
+ * refused); otherwise several CTAs share the walk over a cache and leave their parts there. */
+KDA_API size_t kda_attn_prefill_scratch_bytes(int B, int max_rows, int total_tokens, const kda_dims *dims,
+                                              const kda_kv_cache *cache);
 
 #ifdef __cplusplus
 }

@@ -119,7 +119,8 @@ _SIGS = {
     "kda_kv_append": ([_KV, _I, _VP, _VP, ctypes.c_longlong, _VP, _VP, _I, _I, _VP], _I),
     "kda_attn_decode": ([_KV, _I, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, ctypes.c_size_t, _DIMS, _VP], _I),
     "kda_attn_decode_scratch_bytes": ([_I, _I, _DIMS, _KV], ctypes.c_size_t),
-    "kda_attn_prefill": ([_KV, _I, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _DIMS, _VP], _I),
+    "kda_attn_prefill": ([_KV, _I, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _VP, ctypes.c_size_t, _DIMS, _VP], _I),
+    "kda_attn_prefill_scratch_bytes": ([_I, _I, _I, _DIMS, _KV], ctypes.c_size_t),
 }
 
 
@@ -636,26 +637,39 @@ def kda_attn_decode_scratch_bytes(N: int, K: int, d: KdaDims, cache: KVCache) ->
     return int(lib().kda_attn_decode_scratch_bytes(N, K, ctypes.byref(d), ctypes.byref(cache.struct)))
 
 
+def kda_attn_prefill_scratch_bytes(B: int, max_rows: int, total_tokens: int, d: KdaDims, cache: KVCache) -> int:
+    return int(lib().kda_attn_prefill_scratch_bytes(B, max_rows, total_tokens, ctypes.byref(d),
+                                                    ctypes.byref(cache.struct)))
+
+
+def _attn_scratch(need: int, cache: KVCache, stream_handle: int):
+    """The stream's cached buffer; while the current stream is being captured a buffer of the graph's own, so
+    that graphs captured one after the other may run at once."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.k.device)
+    return scratch_buffer(need, cache.k.device, stream_handle)
+
+
 def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d: KdaDims, window: int = 0,
                     sinks: int = 0, lse=None, stream=None, scratch=None):
     """Attention of the last K tokens of each of N sequences over the cache (q, out [N*K, heads, head_dim] BF16,
-    lse [N*K, heads] F32 or None). `scratch`: the stream's cached buffer when None; while the current stream is
-    being captured a buffer of the graph's own, so that graphs captured one after the other may run at once."""
-    import torch
+    lse [N*K, heads] F32 or None). `scratch`: kda_attn_decode_scratch_bytes bytes; a cached buffer when None."""
     st = _stream(stream)
     if scratch is None:
-        need = kda_attn_decode_scratch_bytes(N, K, d, cache)
-        if torch.cuda.is_current_stream_capturing():
-            scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=cache.k.device)
-        else:
-            scratch = scratch_buffer(need, cache.k.device, st)
+        scratch = _attn_scratch(kda_attn_decode_scratch_bytes(N, K, d, cache), cache, st)
     return _call("kda_attn_decode", ctypes.byref(cache.struct), layer, _p(q), _p(slots), N, K, window, sinks, _p(out),
                  _p(lse), _p(scratch), scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
 
 
 def kda_attn_prefill(cache: KVCache, layer: int, q, cu_seqlens, slots, B: int, max_rows: int, total_tokens: int, out,
-                     d: KdaDims, window: int = 0, sinks: int = 0, lse=None, stream=None):
+                     d: KdaDims, window: int = 0, sinks: int = 0, lse=None, stream=None, scratch=None):
     """Attention of packed rows, the last tokens of their sequences, over the cache (q, out
-    [total_tokens, heads, head_dim] BF16, lse [total_tokens, heads] F32 or None)."""
+    [total_tokens, heads, head_dim] BF16, lse [total_tokens, heads] F32 or None). `scratch` as for
+    kda_attn_decode (kda_attn_prefill_scratch_bytes)."""
+    st = _stream(stream)
+    if scratch is None:
+        scratch = _attn_scratch(kda_attn_prefill_scratch_bytes(B, max_rows, total_tokens, d, cache), cache, st)
     return _call("kda_attn_prefill", ctypes.byref(cache.struct), layer, _p(q), _p(cu_seqlens), _p(slots), B, max_rows,
-                 total_tokens, window, sinks, _p(out), _p(lse), ctypes.byref(d), _stream(stream))
+                 total_tokens, window, sinks, _p(out), _p(lse), _p(scratch),
+                 scratch.numel() * scratch.element_size(), ctypes.byref(d), st)

@@ -31,30 +31,41 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 struct DecodeArgs {
     KvView c;
     const uint16_t *q;
+    const int *cu;  // row bounds of the sequences, or null: K rows each
     const int *slots;
     uint16_t *out;
     float *lse;
     float *part_o, *part_ml;  // [CTA][2][rows][D], [CTA][2][rows][2]
-    long long *info;          // [0] all tiles; then per CTA: pair (n * kv_heads + h), first tile of the pair, tiles of it
+    long long *info;          // [0] all tiles; then per CTA, of the pair that its run starts in: kv head, first tile in the
+                              // list, tiles, first query row, query rows
     int *status;
-    int N, K, G, heads, window, sinks;
+    int N, K, G, heads, window, sinks;  // K: rows per sequence, with cu the most of any
+    int total;                          // with cu: rows of q
     float scale2;  // scale * log2(e)
 };
 
 // The tiles of one sequence: `sink` leading ones, then those from `lo / 64` to the last.
 struct Span {
     int len, lo, sink, tiles;  // tiles = 0: the sequence is skipped
+    int row0, n;               // its query rows
 };
 __device__ __forceinline__ Span span_of(const DecodeArgs &a, int n, bool &bad) {
-    Span s{0, 0, 0, 0};
+    Span s{0, 0, 0, 0, n * a.K, a.K};
     const int slot = a.slots ? a.slots[n] : n;
     bad = true;
+    if (a.cu) {
+        const int c0 = a.cu[n], c1 = a.cu[n + 1];
+        if (c0 < 0 || c1 < c0 || c1 > a.total || c1 - c0 > a.K) return s;
+        s.row0 = c0;
+        s.n = c1 - c0;
+    }
     if (slot < 0 || slot >= a.c.max_seqs) return s;
     const int len = a.c.len[slot];
     if (len < 0 || len > a.c.max_pages * a.c.page_size) return s;
     bad = false;
+    if (s.n == 0) return s;
     s.len = len;
-    s.lo = a.window ? max(0, len - a.K - a.window + 1) : 0;
+    s.lo = a.window ? max(0, len - s.n - a.window + 1) : 0;
     if (s.lo > 0) s.sink = min((min(a.sinks, s.lo) + kTile - 1) / kTile, s.lo / kTile);
     s.tiles = max(1, s.sink + (len + kTile - 1) / kTile - s.lo / kTile);  // an empty one still writes its zeros
     return s;
@@ -124,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
 
     grid_release();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hk = a.c.kv_heads, rows = a.G * a.K;
+    const int hk = a.c.kv_heads, part_rows = a.G * a.K;
 
     // ---- this CTA's run: the tiles of all sequences, summed by the whole block
     const int per = (a.N + kThreads - 1) / kThreads, n_lo = min(a.N, tid * per), n_hi = min(a.N, n_lo + per);
@@ -203,10 +214,12 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     }
     Cursor cc = lc;
     if (tid == 0) {
-        long long *const f = a.info + 1 + 3 * static_cast<long long>(cta);
-        f[0] = static_cast<long long>(lc.n) * hk + lc.h;
+        long long *const f = a.info + 1 + 5 * static_cast<long long>(cta);
+        f[0] = lc.h;
         f[1] = t_begin - lc.i;
         f[2] = lc.s.tiles;
+        f[3] = lc.s.row0;
+        f[4] = lc.s.n;
     }
 
     // ---- loads: each lane l < 64 / page keeps the table entry of the tile's l-th page, one tile ahead
@@ -256,10 +269,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     const int ra = 16 * mt + (lane >> 2), rb = ra + 8;  // this thread's two rows
     uint32_t qf[D / 16][4];
     float o[D / 8][4], m[2], l[2];
-    int pos[2];
+    int pos[2], rows = 0;
     bool seg_bad = false;
     auto begin_pair = [&]() {
-        const uint16_t *const qn = a.q + (static_cast<size_t>(cc.n) * a.K * a.heads + static_cast<size_t>(cc.h) * a.G) * D;
+        rows = a.G * cc.s.n;
+        const uint16_t *const qn = a.q + (static_cast<size_t>(cc.s.row0) * a.heads + static_cast<size_t>(cc.h) * a.G) * D;
         const int ta = ra / a.G, tb = rb / a.G;
         const uint16_t *const qa = qn + (static_cast<size_t>(ta) * a.heads + (ra - ta * a.G)) * D + 2 * (lane & 3);
         const uint16_t *const qb = qn + (static_cast<size_t>(tb) * a.heads + (rb - tb * a.G)) * D + 2 * (lane & 3);
@@ -270,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
             qf[ks][2] = ra < rows ? __ldg(reinterpret_cast<const uint32_t *>(qa + 16 * ks + 8)) : 0u;
             qf[ks][3] = rb < rows ? __ldg(reinterpret_cast<const uint32_t *>(qb + 16 * ks + 8)) : 0u;
         }
-        pos[0] = cc.s.len - a.K + min(ta, a.K - 1);
-        pos[1] = cc.s.len - a.K + min(tb, a.K - 1);
+        pos[0] = cc.s.len - cc.s.n + min(ta, cc.s.n - 1);
+        pos[1] = cc.s.len - cc.s.n + min(tb, cc.s.n - 1);
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
 #pragma unroll
@@ -311,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
             }
         }
         // the whole tile is visible to every row, or each weight is looked at
-        const bool all_seen = j0 + C::KPW <= cc.s.len - a.K + 1 && (!a.window || j0 > cc.s.len - 1 - a.window);
+        const bool all_seen = j0 + C::KPW <= cc.s.len - cc.s.n + 1 && (!a.window || j0 > cc.s.len - 1 - a.window);
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int nb = 0; nb < C::KPW / 8; ++nb) {
@@ -420,14 +434,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
                 if (whole) {
                     if (!seg_bad) {
                         const int tk = r / a.G;
-                        const size_t row = (static_cast<size_t>(cc.n) * a.K + tk) * a.heads + cc.h * a.G + (r - tk * a.G);
+                        const size_t row = static_cast<size_t>(cc.s.row0 + tk) * a.heads + cc.h * a.G + (r - tk * a.G);
                         const float inv = sum == 0.f ? 0.f : 1.f / sum;
                         *reinterpret_cast<uint2 *>(a.out + row * D + d) =
                             make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
                         if (a.lse && d == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top_all + log2f(sum)) * kLn2;
                     }
                 } else {
-                    const size_t pr = (static_cast<size_t>(cta) * 2 + slot) * rows + r;
+                    const size_t pr = (static_cast<size_t>(cta) * 2 + slot) * part_rows + r;
                     *reinterpret_cast<float4 *>(a.part_o + pr * D + d) = v;
                     if (d == 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * pr) = make_float2(top_all, seg_bad ? -1.f : sum);
                 }
@@ -455,8 +469,9 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeA
     const int ctas = static_cast<int>(min(static_cast<long long>(grid_ctas), all));
     const int c = blockIdx.x + 1, r = blockIdx.y, rows = a.G * a.K, tid = threadIdx.x;
     if (c >= ctas) return;
-    const long long *const f = a.info + 1 + 3LL * c;
-    const long long pair = f[0], first = f[1], tiles = f[2];
+    const long long *const f = a.info + 1 + 5LL * c;
+    const long long first = f[1], tiles = f[2];
+    if (r >= a.G * f[4]) return;
     if (run_start(all, ctas, c) == first || run_start(all, ctas, c - 1) > first) return;
     int last = c;
     while (last + 1 < ctas && run_start(all, ctas, last + 1) < first + tiles) ++last;
@@ -486,9 +501,8 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeA
         sum = fmaf(ml.y, w, sum);
         v = fmaf(a.part_o[at(k) * D + tid], w, v);
     }
-    const int n = static_cast<int>(pair / a.c.kv_heads), h = static_cast<int>(pair - static_cast<long long>(n) * a.c.kv_heads);
     const int tk = r / a.G;
-    const size_t row = (static_cast<size_t>(n) * a.K + tk) * a.heads + h * a.G + (r - tk * a.G);
+    const size_t row = static_cast<size_t>(f[3] + tk) * a.heads + f[0] * a.G + (r - tk * a.G);
     a.out[row * D + tid] = f32_to_bf16(sum == 0.f ? 0.f : v / sum);
     if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
@@ -507,17 +521,61 @@ int launch_decode(const DecodeArgs &a, int grid, cudaStream_t s) {
 int ctas_per_sm(int D, int mt) { return D == 64 ? (mt == 4 ? 2 : 3) : 2; }
 int m_tiles(int rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
 
+size_t info_bytes(int grid) { return (1 + 5 * static_cast<size_t>(grid)) * 8 / 16 * 16 + 16; }
+
+}  // namespace
+
+size_t attn_rows_scratch_bytes(int K, int heads, const kda_kv_cache *cache) {
+    const size_t rows = static_cast<size_t>(heads / cache->kv_heads) * K;
+    const int grid = ctas_per_sm(cache->head_dim, m_tiles(static_cast<int>(rows))) * num_sms();
+    return info_bytes(grid) + static_cast<size_t>(grid) * 2 * rows * (cache->head_dim + 4) * sizeof(float);
+}
+
+int attn_rows(const kda_kv_cache *cache, int layer, const uint16_t *q, const int *cu, const int *slots, int N, int K,
+              int total, int window, int sinks, uint16_t *out, float *lse, void *scratch, const kda_dims *dims,
+              cudaStream_t s) {
+    DecodeArgs a{};
+    a.c = kv_view(cache, layer);
+    a.q = q;
+    a.cu = cu;
+    a.slots = slots;
+    a.out = out;
+    a.lse = lse;
+    a.status = device_status_ptr();
+    if (!a.status) return KDA_ERR_CUDA;
+    a.N = N;
+    a.K = K;
+    a.total = total;
+    a.G = dims->heads / cache->kv_heads;
+    a.heads = dims->heads;
+    // a window that holds the longest sequence is none
+    a.window = window < a.c.max_pages * a.c.page_size ? window : 0;
+    a.sinks = std::min(sinks, a.c.max_pages * a.c.page_size);
+    a.scale2 = dims->scale * kLog2e;
+    const int rows = a.G * K, mt = m_tiles(rows), D = dims->head_dim;
+    const int grid = ctas_per_sm(D, mt) * num_sms();
+    char *const p = static_cast<char *>(scratch);
+    a.info = reinterpret_cast<long long *>(p);
+    a.part_o = reinterpret_cast<float *>(p + info_bytes(grid));
+    a.part_ml = a.part_o + static_cast<size_t>(grid) * 2 * rows * D;
+    if (D == 128)
+        return mt == 1 ? launch_decode<128, 1>(a, grid, s)
+                       : (mt == 2 ? launch_decode<128, 2>(a, grid, s) : launch_decode<128, 4>(a, grid, s));
+    return mt == 1 ? launch_decode<64, 1>(a, grid, s)
+                   : (mt == 2 ? launch_decode<64, 2>(a, grid, s) : launch_decode<64, 4>(a, grid, s));
+}
+
+namespace {
+
 int check_shape(int N, int K, const kda_dims *dims, const kda_kv_cache *cache) {
     KDA_TRY(check_cache(cache));
     KDA_TRY(check_dims(dims));
     if (N < 0 || K < 0) return KDA_ERR_INVALID_ARG;
     if (dims->head_dim != cache->head_dim || dims->heads % cache->kv_heads) return KDA_ERR_INVALID_ARG;
-    if (static_cast<long long>(dims->heads / cache->kv_heads) * K > 64) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(dims->heads / cache->kv_heads) * K > kAttnRowsMax) return KDA_ERR_UNSUPPORTED;
     if (static_cast<long long>(N) * K > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
-
-size_t info_bytes(int grid) { return (1 + 3 * static_cast<size_t>(grid)) * 8 / 16 * 16 + 16; }
 
 }  // namespace
 }  // namespace kda
@@ -526,9 +584,7 @@ extern "C" {
 
 size_t kda_attn_decode_scratch_bytes(int N, int K, const kda_dims *dims, const kda_kv_cache *cache) {
     if (kda::check_shape(N, K, dims, cache) != KDA_OK || N == 0 || K == 0) return 0;
-    const size_t rows = static_cast<size_t>(dims->heads / cache->kv_heads) * K;
-    const int grid = kda::ctas_per_sm(dims->head_dim, kda::m_tiles(static_cast<int>(rows))) * kda::num_sms();
-    return kda::info_bytes(grid) + static_cast<size_t>(grid) * 2 * rows * (dims->head_dim + 4) * sizeof(float);
+    return kda::attn_rows_scratch_bytes(K, dims->heads, cache);
 }
 
 int kda_attn_decode(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *slots, int N, int K, int window,
@@ -540,37 +596,9 @@ int kda_attn_decode(const kda_kv_cache *cache, int layer, const kda_bf16 *q, con
     if (N == 0 || K == 0) return KDA_OK;
     if (!scratch) return KDA_ERR_INVALID_ARG;
     if (!kda::aligned16(scratch)) return KDA_ERR_MISALIGNED;
-    if (scratch_bytes < kda_attn_decode_scratch_bytes(N, K, dims, cache)) return KDA_ERR_CAPACITY;
-    kda::DecodeArgs a{};
-    a.c = kda::kv_view(cache, layer);
-    a.q = q;
-    a.slots = slots;
-    a.out = out;
-    a.lse = lse;
-    a.status = kda::device_status_ptr();
-    if (!a.status) return KDA_ERR_CUDA;
-    a.N = N;
-    a.K = K;
-    a.G = dims->heads / cache->kv_heads;
-    a.heads = dims->heads;
-    // a window that holds the longest sequence is none
-    a.window = window < a.c.max_pages * a.c.page_size ? window : 0;
-    a.sinks = std::min(sinks, a.c.max_pages * a.c.page_size);
-    a.scale2 = dims->scale * kda::kLog2e;
-    const int rows = a.G * K, mt = kda::m_tiles(rows), D = dims->head_dim;
-    const int grid = kda::ctas_per_sm(D, mt) * kda::num_sms();
-    char *const p = static_cast<char *>(scratch);
-    a.info = reinterpret_cast<long long *>(p);
-    a.part_o = reinterpret_cast<float *>(p + kda::info_bytes(grid));
-    a.part_ml = a.part_o + static_cast<size_t>(grid) * 2 * rows * D;
-    auto s = static_cast<cudaStream_t>(stream);
-    if (D == 128)
-        return mt == 1   ? kda::launch_decode<128, 1>(a, grid, s)
-               : mt == 2 ? kda::launch_decode<128, 2>(a, grid, s)
-                         : kda::launch_decode<128, 4>(a, grid, s);
-    return mt == 1   ? kda::launch_decode<64, 1>(a, grid, s)
-           : mt == 2 ? kda::launch_decode<64, 2>(a, grid, s)
-                     : kda::launch_decode<64, 4>(a, grid, s);
+    if (scratch_bytes < kda::attn_rows_scratch_bytes(K, dims->heads, cache)) return KDA_ERR_CAPACITY;
+    return kda::attn_rows(cache, layer, q, nullptr, slots, N, K, N * K, window, sinks, out, lse, scratch, dims,
+                          static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

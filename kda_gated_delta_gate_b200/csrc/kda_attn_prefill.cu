@@ -51,6 +51,9 @@ struct PrefillArgs {
     float *lse;
     int *status;
     int B, max_rows, total, heads, G, window, sinks, nslots;
+    int splits;             // CTAs that share a tile's walk; above 1 each leaves a part
+    float *part_o;          // [slot][kv head][split][256][D]
+    float *part_ml;         // [slot][kv head][split][256][2]
     float scale2;  // |scale| log2(e)
     uint32_t flip;  // sign bits of a BF16 pair if scale < 0 (the queries are negated), else 0
 };
@@ -187,16 +190,66 @@ struct Tile {
     int b, slot, c0, n, len, r0;  // r0: first of the 256 rows (token * G + head)
     int lo, hi;                   // visible cached rows: [lo, hi) and those below `sinks`
     int sink;                     // leading tiles that only sinks need
-    int tiles_a, tiles_b;         // per half
+    int all, first;               // tiles of the whole walk; the first of this CTA's part
+    // of this part's tiles i: those below sinks_to start at row 128 (i + first), the others at 128 (i + skip); rows that
+    // no row of the CTA sees are in tiles up to dead_to and from dead_from on
+    int sinks_to, skip, dead_to, dead_from;
+    int tiles_a, tiles_b;         // of this part, per half
+    int rows, base, p_hi_a, p_hi_b;  // rows in the tile, position of the sequence's first query, last positions
 };
 __device__ __forceinline__ int tile_row0(const Tile &t, int i) {
-    return (i < t.sink ? i : i - t.sink + t.lo / kKeys) * kKeys;
+    return (i + (i < t.sinks_to ? t.first : t.skip)) * kKeys;
 }
 
 // Whether cache tile i may have rows that no row of the CTA sees: the last tile, and where a window has
 // passed the start, the sinks' tiles and the window's first.
-__device__ __forceinline__ bool has_dead_rows(const Tile &t, int i, int ntiles) {
-    return i + 1 == ntiles || (t.lo > 0 && i <= t.sink);
+__device__ __forceinline__ bool has_dead_rows(const Tile &t, int i) {
+    return i >= t.dead_from || i <= t.dead_to;
+}
+
+// Finds the 256-row tile of `slot` (all threads call; `found` in shared memory): tiles of sequence b start at slot
+// floor(cu[b] G / 256) + b, which keeps them apart whatever the lengths. False: no such tile, or its sequence
+// is refused. `check`: look every sequence over and latch what is wrong.
+__device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, bool check, int *found, Tile &t) {
+    if (threadIdx.x == 0) *found = 0x7fffffff;
+    __syncthreads();
+    auto first_slot = [&](int b, int c) { return static_cast<long long>(c) * a.G / kRows + b; };
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+        const int c0 = a.cu[b], c1 = a.cu[b + 1];
+        if (first_slot(b, c0) <= slot && slot < first_slot(b + 1, c1)) atomicMin(found, b);
+        if (check) {
+            const int s = a.slots ? a.slots[b] : b;
+            bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.total && c1 - c0 <= a.max_rows && s >= 0 && s < a.c.max_seqs;
+            if (ok) ok = a.c.len[s] >= 0 && a.c.len[s] <= a.c.max_pages * a.c.page_size;
+            if (!ok) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+        }
+    }
+    __syncthreads();
+    t.b = *found;
+    if (t.b >= a.B) return false;
+    t.c0 = a.cu[t.b];
+    const int c1 = a.cu[t.b + 1];
+    t.n = c1 - t.c0;
+    t.slot = a.slots ? a.slots[t.b] : t.b;
+    if (t.c0 < 0 || c1 < t.c0 || c1 > a.total || t.n > a.max_rows || t.slot < 0 || t.slot >= a.c.max_seqs) return false;
+    t.len = a.c.len[t.slot];
+    if (t.len < 0 || t.len > a.c.max_pages * a.c.page_size) return false;
+    const long long r0 = (slot - first_slot(t.b, t.c0)) * kRows, all_rows = static_cast<long long>(t.n) * a.G;
+    if (r0 < 0 || r0 >= all_rows) return false;
+    t.r0 = static_cast<int>(r0);
+    t.rows = static_cast<int>(min(static_cast<long long>(kRows), all_rows - r0));
+    t.base = t.len - t.n;
+    const int p_lo = t.base + t.r0 / a.G;
+    t.p_hi_a = t.base + (t.r0 + min(t.rows, 128) - 1) / a.G;
+    t.p_hi_b = t.base + (t.r0 + t.rows - 1) / a.G;
+    t.lo = a.window ? static_cast<int>(max(0LL, static_cast<long long>(p_lo) - a.window + 1)) : 0;
+    t.hi = t.p_hi_b + 1;
+    t.sink = t.lo > 0 ? min((min(a.sinks, t.lo) + kKeys - 1) / kKeys, t.lo / kKeys) : 0;
+    t.tiles_a = t.p_hi_a < 0 ? 0 : t.sink + t.p_hi_a / kKeys + 1 - t.lo / kKeys;
+    t.tiles_b = t.rows <= 128 || t.p_hi_b < 0 ? 0 : t.sink + t.p_hi_b / kKeys + 1 - t.lo / kKeys;
+    t.all = max(t.tiles_a, t.tiles_b);
+    t.first = 0;
+    return true;
 }
 
 template <int D>
@@ -216,47 +269,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     int *const sfound = const_cast<int *>(bad_page + 1);
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int hk = a.c.kv_heads, h = blockIdx.x % hk;
-    const int slot_id = a.nslots - 1 - static_cast<int>(blockIdx.x / hk);  // the longest walks first
+    const int hk = a.c.kv_heads, split = blockIdx.x % a.splits, h = blockIdx.x / a.splits % hk;
+    const int slot_id = a.nslots - 1 - static_cast<int>(blockIdx.x / a.splits / hk);  // the longest walks first
 
-    // ---- the sequence whose tiles hold this slot: tiles of sequence b start at slot floor(cu[b] G / 256) + b
-    if (tid == 0) *sfound = 0x7fffffff;
-    __syncthreads();
-    auto first_slot = [&](int b, int c) { return static_cast<long long>(c) * a.G / kRows + b; };
-    for (int b = tid; b < a.B; b += kPrefillThreads) {
-        const int c0 = a.cu[b], c1 = a.cu[b + 1];
-        if (first_slot(b, c0) <= slot_id && slot_id < first_slot(b + 1, c1)) atomicMin(sfound, b);
-        if (blockIdx.x == 0) {  // one CTA looks every sequence over
-            const int s = a.slots ? a.slots[b] : b;
-            bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.total && c1 - c0 <= a.max_rows && s >= 0 && s < a.c.max_seqs;
-            if (ok) ok = a.c.len[s] >= 0 && a.c.len[s] <= a.c.max_pages * a.c.page_size;
-            if (!ok) atomicExch(a.status, KDA_ERR_INVALID_ARG);
-        }
-    }
-    __syncthreads();
     Tile t;
-    t.b = *sfound;
-    if (t.b >= a.B) return;
-    t.c0 = a.cu[t.b];
-    const int c1 = a.cu[t.b + 1];
-    t.n = c1 - t.c0;
-    t.slot = a.slots ? a.slots[t.b] : t.b;
-    if (t.c0 < 0 || c1 < t.c0 || c1 > a.total || t.n > a.max_rows || t.slot < 0 || t.slot >= a.c.max_seqs) return;
-    t.len = a.c.len[t.slot];
-    if (t.len < 0 || t.len > a.c.max_pages * a.c.page_size) return;
-    const long long r0 = (slot_id - first_slot(t.b, t.c0)) * kRows, all_rows = static_cast<long long>(t.n) * a.G;
-    if (r0 < 0 || r0 >= all_rows) return;
-    t.r0 = static_cast<int>(r0);
-    const int rows = static_cast<int>(min(static_cast<long long>(kRows), all_rows - r0));
-    const int base = t.len - t.n;  // position of the sequence's first query token
-    const int p_lo = base + t.r0 / a.G;
-    const int p_hi_a = base + (t.r0 + min(rows, 128) - 1) / a.G, p_hi_b = base + (t.r0 + rows - 1) / a.G;  // last positions
-    t.lo = a.window ? static_cast<int>(max(0LL, static_cast<long long>(p_lo) - a.window + 1)) : 0;
-    t.hi = p_hi_b + 1;
-    t.sink = t.lo > 0 ? min((min(a.sinks, t.lo) + kKeys - 1) / kKeys, t.lo / kKeys) : 0;
-    t.tiles_a = p_hi_a < 0 ? 0 : t.sink + p_hi_a / kKeys + 1 - t.lo / kKeys;
-    t.tiles_b = rows <= 128 || p_hi_b < 0 ? 0 : t.sink + p_hi_b / kKeys + 1 - t.lo / kKeys;
-    const int ntiles = max(t.tiles_a, t.tiles_b);
+    if (!locate(a, slot_id, blockIdx.x == 0, sfound, t)) return;
+    t.first = static_cast<int>(static_cast<long long>(t.all) * split / a.splits);
+    const int ntiles = static_cast<int>(static_cast<long long>(t.all) * (split + 1) / a.splits) - t.first;
+    t.sinks_to = t.sink - t.first;
+    t.skip = t.first - t.sink + t.lo / kKeys;
+    t.dead_to = t.lo > 0 ? t.sinks_to : -1;
+    t.dead_from = t.all - 1 - t.first;
+    t.tiles_a = min(max(t.tiles_a - t.first, 0), ntiles);
+    t.tiles_b = min(max(t.tiles_b - t.first, 0), ntiles);
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -283,6 +308,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_release();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp >= 8) {
@@ -332,7 +358,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             __syncwarp();
             if (now.use) tma_load_2d(sm + C::OFF_V + s * C::TILE + off, &a.tv, 64 * half, now.y, &full[s]);
             if (next.use) tma_load_2d(sm + C::OFF_K + (s ^ 1) * C::TILE + off, &a.tk, 64 * half, next.y, &full[s]);
-            if (lane == 0 && has_dead_rows(t, i, ntiles)) mbar_arrive(&fixgo[s]);
+            if (lane == 0 && has_dead_rows(t, i)) mbar_arrive(&fixgo[s]);
             issued = i + 1;
             now = next;
         }
@@ -365,7 +391,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             auto operands = [&](int i) {
                 const int s = i & 1;
                 bool ok = wait_or_abort(&full[s], (i >> 1) & 1, abort, a.status);
-                if (ok && has_dead_rows(t, i, ntiles)) {
+                if (ok && has_dead_rows(t, i)) {
                     ok = wait_or_abort(&vfix[s], (fixes >> s) & 1, abort, a.status);
                     fixes ^= 1u << s;
                 }
@@ -414,7 +440,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
         // full's phase is the tile's own (tiles without such rows pass unseen here)
         uint32_t gone = 0;
         for (int i = 0; i < ntiles; ++i) {
-            if (!has_dead_rows(t, i, ntiles)) continue;
+            if (!has_dead_rows(t, i)) continue;
             uint8_t *const sv = sm + C::OFF_V + (i & 1) * C::TILE;
             if (!wait_or_abort(&fixgo[i & 1], (gone >> (i & 1)) & 1, abort, a.status)) break;
             gone ^= 1u << (i & 1);
@@ -434,10 +460,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- softmax: this thread's row of half x
         const int x = warp >> 2, r = 128 * x + 32 * (warp & 3) + lane;
-        const bool real = r < rows;
+        const bool real = r < t.rows;
         const int tok = (t.r0 + r) / a.G, g = t.r0 + r - tok * a.G;
         const size_t row = static_cast<size_t>(t.c0 + (real ? tok : 0)) * a.heads + static_cast<size_t>(h) * a.G + (real ? g : 0);
-        const int pos = base + min(tok, t.n - 1);
+        const int pos = t.base + min(tok, t.n - 1);
         {
             const uint4 *const src = reinterpret_cast<const uint4 *>(a.q + row * D);
             uint8_t *const dst = sm + x * C::TILE;
@@ -455,7 +481,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             if (lane == 0) mbar_arrive(qfull);
         }
         const uint32_t ts = tmem_lane_base(tmem, warp) + 128 * x, to = tmem_lane_base(tmem, warp) + 256 + 128 * x;
-        const int p_first = base + (t.r0 + 128 * x) / a.G, p_last = x ? p_hi_b : p_hi_a, tiles = x ? t.tiles_b : t.tiles_a;
+        const int p_first = t.base + (t.r0 + 128 * x) / a.G, p_last = x ? t.p_hi_b : t.p_hi_a, tiles = x ? t.tiles_b : t.tiles_a;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int i = 0; i < tiles; ++i) {
@@ -533,7 +559,22 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
         }
         if (ok && tiles > 0) ok = wait_or_abort(&ofull[x], 0, abort, a.status);
         tc_fence_after();
-        if (ok && !*bad_page) {
+        if (a.splits > 1) {  // this part's l, m and unscaled O; l = -1: a page was none
+            const size_t pr = (static_cast<size_t>(slot_id) * hk + h) * a.splits * kRows + static_cast<size_t>(split) * kRows + r;
+            float4 *const dst = reinterpret_cast<float4 *>(a.part_o + pr * D);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(to + c, o);
+                tmem_ld_wait();
+                if (real && l != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) dst[(c + e) / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+            *reinterpret_cast<float2 *>(a.part_ml + 2 * pr) = make_float2(m, ok && !*bad_page ? l : -1.f);
+            if (*bad_page && tid == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+        } else if (ok && !*bad_page) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
             uint4 *const dst = reinterpret_cast<uint4 *>(a.out + row * D);
 #pragma unroll
@@ -563,6 +604,62 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
+// The parts of split walks, added in order; one warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PrefillArgs a) {
+    constexpr int E = D / 32;
+    __shared__ int found;
+    grid_acquire();
+    const int hk = a.c.kv_heads, h = blockIdx.x % hk, slot = blockIdx.x / hk, lane = threadIdx.x & 31;
+    Tile t;
+    if (!locate(a, slot, false, &found, t)) return;
+    const float *const ml = a.part_ml + 2 * (static_cast<size_t>(slot) * hk + h) * a.splits * kRows;
+    const float *const po = a.part_o + (static_cast<size_t>(slot) * hk + h) * a.splits * kRows * D;
+    const int r = 8 * blockIdx.y + (threadIdx.x >> 5);
+    if (r >= t.rows) return;
+    float m = -INFINITY;
+    bool bad = false;
+    for (int p = 0; p < a.splits; ++p) {
+        m = fmaxf(m, ml[2 * (p * kRows + r)]);
+        bad |= ml[2 * (p * kRows + r) + 1] == -1.f;
+    }
+    // a page that is none leaves the whole tile, as an unsplit walk does
+    for (int p = 0; p < a.splits; ++p)
+        for (int k = lane; k < t.rows; k += 32) bad |= ml[2 * (p * kRows + k) + 1] == -1.f;
+    if (__any_sync(0xffffffffu, bad)) return;
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < a.splits; ++p) {
+        const float lp = ml[2 * (p * kRows + r) + 1];
+        if (lp == 0.f) continue;  // that part saw nothing and left no O
+        const float w = ex2(ml[2 * (p * kRows + r)] - m);
+        l = fmaf(lp, w, l);
+        const float *const src = po + (static_cast<size_t>(p) * kRows + r) * D + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], w, o[e]);
+    }
+    const int q = t.r0 + r, tok = q / a.G;
+    const size_t row = static_cast<size_t>(t.c0 + tok) * a.heads + static_cast<size_t>(h) * a.G + (q - tok * a.G);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t u[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) u[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
+    uint16_t *const dst = a.out + row * D + E * lane;
+    if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(u[0], u[1]);
+    else *reinterpret_cast<uint32_t *>(dst) = u[0];
+    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// CTAs that share the walk of one (256-row tile, kv head): enough that all walks together fill the SMs, at most 16, and
+// none shorter than two tiles of the longest cache. total_tokens G / 256 tiles, or one per sequence, are the fewest there are.
+int prefill_splits(int B, int total, int G, const kda_kv_cache *c) {
+    const long long fewest = std::max<long long>(std::min(B, total), (static_cast<long long>(total) * G + kRows - 1) / kRows);
+    const long long tiles = (static_cast<long long>(c->max_pages) * c->page_size + kKeys - 1) / kKeys;
+    return static_cast<int>(std::max<long long>(1, std::min<long long>({16, num_sms() / (fewest * c->kv_heads), tiles / 2})));
+}
+
 // 2-D map over a layer's pool as rows of D values; boxes of 64 channels x min(page, 128) rows.
 int make_pool_map(CUtensorMap *tm, const void *base, const KvView &c, int D) {
     EncodeTiledFn fn = encode_fn();
@@ -581,31 +678,76 @@ template <int D>
 int launch_prefill(const PrefillArgs &a, unsigned grid, cudaStream_t s) {
     static std::atomic<unsigned long long> attr{0};
     KDA_TRY(smem_opt_in(prefill_kernel<D>, PrefillCfg<D>::BYTES, attr));
-    prefill_kernel<D><<<grid, kPrefillThreads, PrefillCfg<D>::BYTES, s>>>(a);
-    return launch_status();
+    prefill_kernel<D><<<grid * a.splits, kPrefillThreads, PrefillCfg<D>::BYTES, s>>>(a);
+    KDA_TRY(launch_status());
+    if (a.splits == 1) return KDA_OK;
+    return launch_after(prefill_join_kernel<D>, dim3(grid, kRows / 8), dim3(256), 0, s, a);
 }
 
 }  // namespace
 }  // namespace kda
 
-extern "C" int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *cu_seqlens,
-                                const int *slots, int B, int max_rows, int total_tokens, int window, int sinks,
-                                kda_bf16 *out, float *lse, const kda_dims *dims, void *stream) {
-    KDA_TRY(kda::check_cache(cache));
-    KDA_TRY(kda::check_dims(dims));
-    if (!q || !cu_seqlens || !out || B < 0 || max_rows < 0 || total_tokens < 0 || window < 0 || sinks < 0 || layer < 0 ||
-        layer >= cache->layers)
-        return KDA_ERR_INVALID_ARG;
+namespace kda {
+namespace {
+
+int check_prefill(int B, int max_rows, int total, const kda_dims *dims, const kda_kv_cache *cache) {
+    KDA_TRY(check_cache(cache));
+    KDA_TRY(check_dims(dims));
+    if (B < 0 || max_rows < 0 || total < 0) return KDA_ERR_INVALID_ARG;
     if (dims->head_dim != cache->head_dim || dims->heads % cache->kv_heads) return KDA_ERR_INVALID_ARG;
-    if (!kda::aligned16(q) || !kda::aligned16(out)) return KDA_ERR_MISALIGNED;
     if (B > 65535 || dims->heads > 65535) return KDA_ERR_UNSUPPORTED;
+    const int G = dims->heads / cache->kv_heads;
+    const long long slots = static_cast<long long>(total) * G / kRows + B;
+    if (static_cast<long long>(total) * G > 0x7fffffffLL - kRows || slots * cache->kv_heads > 0x7fffffffLL)
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// Few rows per sequence go to the split form on mma.sync, whose CTAs share the cache evenly (8 sequences of at most 4 rows
+// over 2000 tokens: see the file's head for both); the rest here.
+bool few_rows(int max_rows, const kda_dims *dims, const kda_kv_cache *cache) {
+    return static_cast<long long>(dims->heads / cache->kv_heads) * max_rows <= kAttnRowsMax;
+}
+
+}  // namespace
+}  // namespace kda
+
+extern "C" {
+
+size_t kda_attn_prefill_scratch_bytes(int B, int max_rows, int total_tokens, const kda_dims *dims,
+                                      const kda_kv_cache *cache) {
+    if (kda::check_prefill(B, max_rows, total_tokens, dims, cache) != KDA_OK || B == 0 || total_tokens == 0 || max_rows == 0)
+        return 0;
+    if (kda::few_rows(max_rows, dims, cache)) return kda::attn_rows_scratch_bytes(max_rows, dims->heads, cache);
+    const int G = dims->heads / cache->kv_heads, splits = kda::prefill_splits(B, total_tokens, G, cache);
+    if (splits == 1) return 0;
+    const size_t slots = static_cast<size_t>(total_tokens) * G / kda::kRows + B;
+    return slots * cache->kv_heads * splits * kda::kRows * (cache->head_dim + 4) * sizeof(float);
+}
+
+int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *cu_seqlens, const int *slots,
+                     int B, int max_rows, int total_tokens, int window, int sinks, kda_bf16 *out, float *lse,
+                     void *scratch, size_t scratch_bytes, const kda_dims *dims, void *stream) {
+    KDA_TRY(kda::check_prefill(B, max_rows, total_tokens, dims, cache));
+    if (!q || !cu_seqlens || !out || window < 0 || sinks < 0 || layer < 0 || layer >= cache->layers)
+        return KDA_ERR_INVALID_ARG;
+    if (!kda::aligned16(q) || !kda::aligned16(out)) return KDA_ERR_MISALIGNED;
     if (B == 0 || total_tokens == 0) return KDA_OK;
     if (max_rows == 0) return KDA_ERR_INVALID_ARG;
+    const size_t need = kda_attn_prefill_scratch_bytes(B, max_rows, total_tokens, dims, cache);
+    if (need) {
+        if (!scratch) return KDA_ERR_INVALID_ARG;
+        if (!kda::aligned16(scratch)) return KDA_ERR_MISALIGNED;
+        if (scratch_bytes < need) return KDA_ERR_CAPACITY;
+    }
+    auto s = static_cast<cudaStream_t>(stream);
+    if (kda::few_rows(max_rows, dims, cache))
+        return kda::attn_rows(cache, layer, q, cu_seqlens, slots, B, max_rows, total_tokens, window, sinks, out, lse,
+                              scratch, dims, s);
     kda::PrefillArgs a{};
     a.G = dims->heads / cache->kv_heads;
-    const long long slots_n = static_cast<long long>(total_tokens) * a.G / kda::kRows + B;
-    if (static_cast<long long>(total_tokens) * a.G > 0x7fffffffLL - kda::kRows || slots_n * cache->kv_heads > 0x7fffffffLL)
-        return KDA_ERR_UNSUPPORTED;
+    a.nslots = static_cast<int>(static_cast<long long>(total_tokens) * a.G / kda::kRows + B);
+    a.splits = kda::prefill_splits(B, total_tokens, a.G, cache);
     a.status = kda::device_status_ptr();
     if (!a.status) return KDA_ERR_CUDA;
     a.c = kda::kv_view(cache, layer);
@@ -623,11 +765,13 @@ extern "C" int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_
     // a window that holds the longest sequence is none
     a.window = window < a.c.max_pages * a.c.page_size ? window : 0;
     a.sinks = std::min(sinks, a.c.max_pages * a.c.page_size);
-    a.nslots = static_cast<int>(slots_n);
     // a negative scale is taken as negated queries, and 0 as one so small that every weight is 1
     a.scale2 = std::max(std::fabs(dims->scale) * 1.4426950408889634f, 1e-30f);
     a.flip = dims->scale < 0.f ? 0x80008000u : 0u;
-    const unsigned grid = static_cast<unsigned>(slots_n * cache->kv_heads);
-    auto s = static_cast<cudaStream_t>(stream);
+    a.part_o = static_cast<float *>(scratch);
+    a.part_ml = a.part_o + static_cast<size_t>(a.nslots) * cache->kv_heads * a.splits * kda::kRows * cache->head_dim;
+    const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.nslots) * cache->kv_heads);
     return cache->head_dim == 128 ? kda::launch_prefill<128>(a, grid, s) : kda::launch_prefill<64>(a, grid, s);
 }
+
+}  // extern "C"

@@ -67,4 +67,12 @@ int launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaS
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+// Attention of a few query rows per sequence, split over the cached rows (kda_attn_decode.cu): K rows of each
+// sequence, or with cu (device, row bounds) at most K. heads / kv_heads * K <= kAttnRowsMax; scratch as sized.
+constexpr int kAttnRowsMax = 64;
+size_t attn_rows_scratch_bytes(int K, int heads, const kda_kv_cache *cache);
+int attn_rows(const kda_kv_cache *cache, int layer, const uint16_t *q, const int *cu, const int *slots, int N, int K,
+              int total, int window, int sinks, uint16_t *out, float *lse, void *scratch, const kda_dims *dims,
+              cudaStream_t s);
+
 }  // namespace kda

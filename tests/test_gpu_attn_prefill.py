@@ -45,6 +45,13 @@ CASES = [
     ([900, 640], [100, 300], 4, 1, 64, 64, 130, 200),
     ([1500, 20], [70, 20], 4, 2, 128, 16, 257, 129),
     ([600], [600], 4, 2, 128, 64, 5000, 7),
+    ([700, 900], [700, 900], 16, 8, 64, 32, 0, 0),                # enough rows for one CTA per walk
+    ([700, 400], [700, 400], 24, 8, 128, 64, 200, 3),
+    ([9000, 40], [300, 2], 8, 2, 128, 64, 0, 0),                  # a chunk behind many cached tokens: shared walks
+    ([5000], [130], 2, 1, 64, 16, 2000, 10),
+    ([300, 7, 0, 900, 64], [3, 0, 2, 1, 4], 8, 2, 128, 16, 0, 0),  # few rows per sequence
+    ([300, 7, 0, 900, 64], [3, 0, 5, 16, 4], 8, 2, 64, 32, 40, 2),
+    ([200, 1000], [64, 1], 4, 4, 128, 16, 0, 0),
 ]
 
 
@@ -109,6 +116,45 @@ def test_bad_sequences_and_rows_behind_the_last_are_left():
         assert kda.device_status(clear=True) == 1
     out, lse = run(c, cu=i32([0, 0, 130, 130, 130, 130]), slots=i32([3, 1, 1, 1, 3]))
     assert torch.isnan(out[130:]).all() and torch.isnan(lse[130:]).all() and not torch.isnan(out[:130]).any()
+
+
+def test_bad_sequences_of_few_rows():
+    c = Case([300, 130, 64, 90, 200], [3, 2, 4, 1, 2], 4, 2, 64, 16, seed=12)
+    o = c.expected()
+    hit = lambda i: slice(c.cu[i], c.cu[i + 1])
+    c.cache.seq_len[2] = 10 ** 9
+    c.cache.page_table[0, 3] = -3
+    out, lse = run(c)
+    assert kda.device_status(clear=True) == 1
+    for i in range(5):
+        if i in (0, 2):
+            assert torch.isnan(out[hit(i)]).all() and torch.isnan(lse[hit(i)]).all()
+        else:
+            check(out[hit(i)], lse[hit(i)], tuple(x[hit(i)] for x in o))
+    for cu in ([0, 6, 4, 4, 4, 5], [-7, 1, 1, 1, 1, 1], [0, 0, 0, 0, 0, 10 ** 6], [2 ** 31 - 1, -2 ** 31, 0, 0, 0, 0]):
+        run(c, cu=i32(cu), slots=i32([1] * 5))
+        assert kda.device_status(clear=True) == 1
+    out, lse = run(c, cu=i32([0, 0, 2, 2, 2, 3]), slots=i32([3, 1, 1, 1, 3]))
+    assert torch.isnan(out[3:]).all() and not torch.isnan(out[:3]).any()
+
+
+def test_a_bad_page_in_one_part_of_a_shared_walk_leaves_the_tile():
+    c = Case([6000, 500], [100, 100], 4, 2, 64, 16, seed=13)
+    o = c.expected()
+    c.cache.page_table[0, 200] = 10 ** 8
+    out, lse = run(c)
+    assert kda.device_status(clear=True) == 1
+    assert torch.isnan(out[:100]).all() and torch.isnan(lse[:100]).all()
+    check(out[100:], lse[100:], tuple(x[100:] for x in o))
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+@pytest.mark.parametrize("rows", [[300, 40], [7, 3]])
+def test_negative_and_zero_scales(scale, rows):
+    c = Case([300, 40], rows, 8, 2, 64, 16, seed=14)
+    c.scale = scale
+    c.d = kda.dims(8, 64, scale=scale)
+    check(*run(c), c.expected())
 
 
 def test_far_pages():

@@ -39,8 +39,8 @@ def test_every_call_refuses_a_bad_cache(L, kw, code):
     assert L.kda_kv_compact(c, None, None) == code
     assert L.kda_kv_append(c, 0, BOGUS, BOGUS, 128, BOGUS, BOGUS, 1, 1, None) == code
     assert L.kda_attn_decode(c, 0, BOGUS, None, 1, 1, 0, 0, BOGUS, None, BOGUS, 1 << 30, d, None) == code
-    assert L.kda_attn_prefill(c, 0, BOGUS, BOGUS, None, 1, 1, 1, 0, 0, BOGUS, None, d, None) == code
-    assert L.kda_attn_decode_scratch_bytes(1, 1, d, c) == 0
+    assert L.kda_attn_prefill(c, 0, BOGUS, BOGUS, None, 1, 1, 1, 0, 0, BOGUS, None, BOGUS, 1 << 30, d, None) == code
+    assert L.kda_attn_decode_scratch_bytes(1, 1, d, c) == 0 == L.kda_attn_prefill_scratch_bytes(1, 1, 1, d, c)
 
 
 def test_bookkeeping_arguments(L):
@@ -78,8 +78,9 @@ def test_attention_arguments(L):
     def dec(c=None, layer=0, q=BOGUS, N=1, K=1, w=0, s=0, out=BOGUS, scr=BOGUS, nb=1 << 30, dims=dp):
         return L.kda_attn_decode(c or _c(), layer, q, None, N, K, w, s, out, None, scr, nb, dims, None)
 
-    def pre(c=None, layer=0, q=BOGUS, cu=BOGUS, B=1, rows=1, total=1, w=0, s=0, out=BOGUS, dims=dp):
-        return L.kda_attn_prefill(c or _c(), layer, q, cu, None, B, rows, total, w, s, out, None, dims, None)
+    def pre(c=None, layer=0, q=BOGUS, cu=BOGUS, B=1, rows=1, total=1, w=0, s=0, out=BOGUS, scr=BOGUS, nb=1 << 30,
+            dims=dp):
+        return L.kda_attn_prefill(c or _c(), layer, q, cu, None, B, rows, total, w, s, out, None, scr, nb, dims, None)
 
     for f in (dec, pre):
         assert f(layer=2) == 1 and f(layer=-1) == 1 and f(q=None) == 1 and f(out=None) == 1
@@ -94,6 +95,10 @@ def test_attention_arguments(L):
     assert need > 0 and L.kda_attn_decode_scratch_bytes(0, 1, dp, _c()) == 0
     assert dec(scr=None) == 1 and dec(scr=BOGUS + 8) == 7 and dec(nb=need - 16) == 3
     assert pre(cu=None) == 1 and pre(B=-1) == 1 and pre(rows=-1) == 1 and pre(total=-1) == 1
+    need = L.kda_attn_prefill_scratch_bytes(1, 1, 1, dp, _c())
+    assert need > 0 and L.kda_attn_prefill_scratch_bytes(0, 1, 1, dp, _c()) == 0
+    assert L.kda_attn_prefill_scratch_bytes(1, 50000, 50000, dp, _c()) == 0  # the rows fill the SMs
+    assert pre(scr=None) == 1 and pre(scr=BOGUS + 8) == 7 and pre(nb=need - 16) == 3
     assert pre(B=0) == 0 and pre(total=0) == 0 and pre(rows=0) == 1 and pre(B=70000) == 4
 
 
