@@ -106,8 +106,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// Tile runs: CTA c of `ctas` takes tiles [run_start(c), run_start(c + 1)).
-__device__ __forceinline__ long long run_start(long long tiles, int ctas, int c) { return tiles * c / ctas; }
+// Tile runs: CTA c of `ctas` (below 1024) takes tiles [run_start(c), run_start(c + 1)).
+__device__ __forceinline__ long long run_start(long long tiles, int ctas, int c) {
+    if (tiles < (1 << 22)) return static_cast<unsigned>(tiles) * static_cast<unsigned>(c) / static_cast<unsigned>(ctas);
+    return tiles * c / ctas;
+}
+// The run that holds tile x: the last c with tiles c / ctas < x + 1.
+__device__ __forceinline__ int run_of(long long tiles, int ctas, long long x) {
+    return static_cast<int>(((x + 1) * ctas + tiles - 1) / tiles) - 1;
+}
 
 template <int D, int MT>
 struct DecodeCfg {
@@ -116,8 +123,11 @@ struct DecodeCfg {
     static constexpr int STAGES = D == 64 ? 4 : (MT == 4 ? 2 : 3);
     static constexpr int HALF = kTile * D * 2;    // bytes of a tile's K (or V)
     static constexpr int ROWS = 16 * MT;
-    static constexpr int OFF_O = STAGES * 2 * HALF;            // [ROWS][D] FP32
-    static constexpr int OFF_ML = OFF_O + ROWS * D * 4;        // [KG][ROWS][2]
+    // row stride of the join buffer: eight channels more put the eight rows that a warp writes at once on
+    // different banks; two CTAs of 32 rows just fit an SM with two more
+    static constexpr int OD = D + (MT == 2 ? 2 : 8);
+    static constexpr int OFF_O = STAGES * 2 * HALF;            // [ROWS][OD] FP32
+    static constexpr int OFF_ML = OFF_O + ROWS * OD * 4;       // [KG][ROWS][2]
     static constexpr int OFF_MISC = OFF_ML + KG * ROWS * 8;    // scan, cursor, flags
     static constexpr int BYTES = OFF_MISC + 256;
     static constexpr int CTAS = D == 64 ? (MT == 4 ? 2 : 3) : 2;  // resident per SM
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     open(lc);
     {
         const long long in = t_begin - scur[1];
-        lc.h = static_cast<int>(in / lc.s.tiles);
+        lc.h = in < (1LL << 31) ? static_cast<int>(in) / lc.s.tiles : static_cast<int>(in / lc.s.tiles);
         lc.i = static_cast<int>(in - static_cast<long long>(lc.h) * lc.s.tiles);
     }
     Cursor cc = lc;
@@ -269,10 +279,11 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     const int ra = 16 * mt + (lane >> 2), rb = ra + 8;  // this thread's two rows
     uint32_t qf[D / 16][4];
     float o[D / 8][4], m[2], l[2];
-    int pos[2], rows = 0;
+    int pos[2];
     bool seg_bad = false;
-    auto begin_pair = [&]() {
-        rows = a.G * cc.s.n;
+    // the rows' queries and positions; called before the last pair's results are written, so that the loads run under that
+    auto fetch_rows = [&]() {
+        const int rows = a.G * cc.s.n;
         const uint16_t *const qn = a.q + (static_cast<size_t>(cc.s.row0) * a.heads + static_cast<size_t>(cc.h) * a.G) * D;
         const int ta = ra / a.G, tb = rb / a.G;
         const uint16_t *const qa = qn + (static_cast<size_t>(ta) * a.heads + (ra - ta * a.G)) * D + 2 * (lane & 3);
@@ -286,6 +297,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
         }
         pos[0] = cc.s.len - cc.s.n + min(ta, cc.s.n - 1);
         pos[1] = cc.s.len - cc.s.n + min(tb, cc.s.n - 1);
+    };
+    auto begin_pair = [&]() {
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
 #pragma unroll
@@ -297,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     for (int s = 0; s < C::STAGES - 1; ++s) load(s);
     int stage = 0;
     long long seg0 = t_begin;  // where the current pair's tiles in this run begin
+    fetch_rows();
     begin_pair();
 #pragma unroll 1
     for (long long t = t_begin; t < t_end; ++t) {
@@ -384,6 +398,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
 
         // ---- the pair's last tile of this run: join the warps, then write the result or this run's part
         if (cc.i + 1 == cc.s.tiles || t + 1 == t_end) {
+            const long long pair0 = t - cc.i;  // the pair's first tile in the list
+            const bool whole = pair0 >= t_begin && cc.i + 1 == cc.s.tiles;
+            const int slot = seg0 == t_begin ? 0 : 1, rows = a.G * cc.s.n, h = cc.h, row0 = cc.s.row0;
+            if (t + 1 < t_end) {
+                step(cc);
+                fetch_rows();
+                seg0 = t + 1;
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -400,59 +422,55 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
                 f[e] = ex2(m[e] - (top_all == -INFINITY ? 0.f : top_all));
             }
 #pragma unroll
-            for (int g = 0; g < C::KG; ++g) {
+            for (int g = 0; g < C::KG; ++g) {  // in key order; a warp's loads all go out before its stores
                 if (kg == g) {
 #pragma unroll
-                    for (int d = 0; d < D / 8; ++d) {
+                    for (int e = 0; e < 2; ++e) {
+                        float *const w = so + (e ? rb : ra) * C::OD + 2 * (lane & 3);
+                        float2 u[D / 8];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float2 *const w = reinterpret_cast<float2 *>(so + (e ? rb : ra) * D + 8 * d + 2 * (lane & 3));
-                            float2 v = make_float2(o[d][2 * e] * f[e], o[d][2 * e + 1] * f[e]);
-                            if (g) {
-                                const float2 u = *w;
-                                v.x += u.x;
-                                v.y += u.y;
-                            }
-                            *w = v;
-                        }
+                        for (int d = 0; d < D / 8; ++d)
+                            u[d] = g ? *reinterpret_cast<const float2 *>(w + 8 * d) : make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int d = 0; d < D / 8; ++d)
+                            *reinterpret_cast<float2 *>(w + 8 * d) =
+                                make_float2(fmaf(o[d][2 * e], f[e], u[d].x), fmaf(o[d][2 * e + 1], f[e], u[d].y));
                     }
                 }
                 __syncthreads();
             }
-            const long long pair0 = t - cc.i;  // the pair's first tile in the list
-            const bool whole = pair0 >= t_begin && cc.i + 1 == cc.s.tiles;
-            const int slot = seg0 == t_begin ? 0 : 1;
             for (int i = tid; i < rows * (D / 4); i += kThreads) {
                 const int r = i / (D / 4), d = 4 * (i % (D / 4));
                 float top_all = -INFINITY, sum = 0.f;
+                float2 ml[C::KG];
 #pragma unroll
-                for (int g = 0; g < C::KG; ++g) top_all = fmaxf(top_all, sml[g * C::ROWS + r].x);
+                for (int g = 0; g < C::KG; ++g) {
+                    ml[g] = sml[g * C::ROWS + r];
+                    top_all = fmaxf(top_all, ml[g].x);
+                }
                 const float ref = top_all == -INFINITY ? 0.f : top_all;
 #pragma unroll
-                for (int g = 0; g < C::KG; ++g) sum += sml[g * C::ROWS + r].y * ex2(sml[g * C::ROWS + r].x - ref);
-                const float4 v = *reinterpret_cast<const float4 *>(so + r * D + d);
+                for (int g = 0; g < C::KG; ++g) sum += ml[g].y * ex2(ml[g].x - ref);
+                const float *const sv = so + r * C::OD + d;
+                const float2 v0 = *reinterpret_cast<const float2 *>(sv), v1 = *reinterpret_cast<const float2 *>(sv + 2);
                 if (whole) {
                     if (!seg_bad) {
                         const int tk = r / a.G;
-                        const size_t row = static_cast<size_t>(cc.s.row0 + tk) * a.heads + cc.h * a.G + (r - tk * a.G);
+                        const size_t row = static_cast<size_t>(row0 + tk) * a.heads + h * a.G + (r - tk * a.G);
                         const float inv = sum == 0.f ? 0.f : 1.f / sum;
                         *reinterpret_cast<uint2 *>(a.out + row * D + d) =
-                            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+                            make_uint2(pack_bf16(v0.x * inv, v0.y * inv), pack_bf16(v1.x * inv, v1.y * inv));
                         if (a.lse && d == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top_all + log2f(sum)) * kLn2;
                     }
                 } else {
                     const size_t pr = (static_cast<size_t>(cta) * 2 + slot) * part_rows + r;
-                    *reinterpret_cast<float4 *>(a.part_o + pr * D + d) = v;
+                    *reinterpret_cast<float4 *>(a.part_o + pr * D + d) = make_float4(v0.x, v0.y, v1.x, v1.y);
                     if (d == 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * pr) = make_float2(top_all, seg_bad ? -1.f : sum);
                 }
             }
             if (seg_bad && tid == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
             __syncthreads();  // so and sml are read; the next pair may overwrite them
-            if (t + 1 < t_end) {
-                step(cc);
-                seg0 = t + 1;
-                begin_pair();
-            }
+            begin_pair();
         } else {
             ++cc.i;
         }
@@ -460,51 +478,73 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Block (c - 1, r): row r of the pair that the cut between runs c - 1 and c splits, if it is the pair's first cut.
+// Block (c - 1, r): row r of the pair that the cut between runs c - 1 and c splits, if it is the pair's first
+// cut. Four warps take every fourth part each and their sums are added in warp order.
+constexpr int kJoinWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ DecodeArgs a, int grid_ctas) {
-    __shared__ float sw[D / 32];
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ DecodeArgs a, int grid_ctas) {
+    constexpr int E = D / 32;
+    __shared__ float so[kJoinWarps][D], ss[kJoinWarps];
     grid_acquire();
     const long long all = a.info[0];
     const int ctas = static_cast<int>(min(static_cast<long long>(grid_ctas), all));
-    const int c = blockIdx.x + 1, r = blockIdx.y, rows = a.G * a.K, tid = threadIdx.x;
+    const int c = blockIdx.x + 1, r = blockIdx.y, rows = a.G * a.K, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (c >= ctas) return;
     const long long *const f = a.info + 1 + 5LL * c;
     const long long first = f[1], tiles = f[2];
-    if (r >= a.G * f[4]) return;
-    if (run_start(all, ctas, c) == first || run_start(all, ctas, c - 1) > first) return;
-    int last = c;
-    while (last + 1 < ctas && run_start(all, ctas, last + 1) < first + tiles) ++last;
-    const int slot0 = run_start(all, ctas, c - 1) == first ? 0 : 1;
+    if (r >= a.G * f[4] || run_start(all, ctas, c) == first) return;
+    const long long before = run_start(all, ctas, c - 1);
+    if (before > first) return;
+    const int last = run_of(all, ctas, first + tiles - 1), slot0 = before == first ? 0 : 1;
     auto at = [&](int k) { return (static_cast<size_t>(k) * 2 + (k == c - 1 ? slot0 : 0)) * rows + r; };
 
     // the largest m of the parts, and whether one of them met a bad page
     float top = -INFINITY;
     bool bad = false;
-    for (int k = c - 1 + tid; k <= last; k += D) {
+    for (int k = c - 1 + lane; k <= last; k += 32) {
         const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at(k));
         top = fmaxf(top, ml.x);
         bad |= ml.y == -1.f;
     }
+    if (__any_sync(0xffffffffu, bad)) return;  // the same in every warp
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((tid & 31) == 0) sw[tid >> 5] = top;
-    if (__syncthreads_or(bad)) return;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) top = fmaxf(top, sw[w]);
     const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, v = 0.f;
+    float sum = 0.f, v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll 4
-    for (int k = c - 1; k <= last; ++k) {
+    for (int k = c - 1 + warp; k <= last; k += kJoinWarps) {
         const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at(k));
+        const float *const src = a.part_o + at(k) * D + E * lane;
+        float x[E];
+        if constexpr (E == 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(src);
+            x[0] = q.x, x[1] = q.y, x[2] = q.z, x[3] = q.w;
+        } else {
+            const float2 q = *reinterpret_cast<const float2 *>(src);
+            x[0] = q.x, x[1] = q.y;
+        }
         const float w = ex2(ml.x - ref);
         sum = fmaf(ml.y, w, sum);
-        v = fmaf(a.part_o[at(k) * D + tid], w, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = fmaf(x[e], w, v[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][E * lane + e] = v[e];
+    if (lane == 0) ss[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x >= D) return;  // D <= 32 kJoinWarps
+    float o = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        o += so[w][threadIdx.x];
+        l += ss[w];
     }
     const int tk = r / a.G;
     const size_t row = static_cast<size_t>(f[3] + tk) * a.heads + f[0] * a.G + (r - tk * a.G);
-    a.out[row * D + tid] = f32_to_bf16(sum == 0.f ? 0.f : v / sum);
-    if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    a.out[row * D + threadIdx.x] = f32_to_bf16(l == 0.f ? 0.f : o / l);
+    if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 template <int D, int MT>
@@ -515,7 +555,7 @@ int launch_decode(const DecodeArgs &a, int grid, cudaStream_t s) {
     decode_kernel<D, MT><<<grid, kThreads, C::BYTES, s>>>(a);
     KDA_TRY(launch_status());
     if (grid < 2) return KDA_OK;
-    return launch_after(join_kernel<D>, dim3(grid - 1, a.G * a.K), dim3(D), 0, s, a, grid);
+    return launch_after(join_kernel<D>, dim3(grid - 1, a.G * a.K), dim3(32 * kJoinWarps), 0, s, a, grid);
 }
 
 int ctas_per_sm(int D, int mt) { return D == 64 ? (mt == 4 ? 2 : 3) : 2; }
