@@ -722,8 +722,8 @@ KDA_API int kda_kv_append(const kda_kv_cache *cache, int layer, const kda_bf16 *
  *   slots  DEVICE int32 [N] or NULL (slot n); a slot may be listed more than once
  *   dims   heads, head_dim (the cache's) and scale (the score scale, e.g. 1/sqrt(head_dim))
  *   window 0 (none) or >= 1, the query's own token counted;  sinks >= 0
- *   scratch  at least kda_attn_decode_scratch_bytes(N, K, dims, cache) bytes, 16-byte aligned: partial
- *          results of cache ranges that several CTAs share; contents on entry do not matter
+ *   scratch  at least kda_attn_decode_scratch_bytes(N, K, dims, cache) bytes, 16-byte aligned (NULL where that is
+ *          0): partial results of cache ranges that several CTAs share; contents on entry do not matter
  * heads / kv_heads * K <= 64 (else KDA_ERR_UNSUPPORTED: use kda_attn_prefill). The rows of a
  * sequence with a slot out of range or a length that is negative or past max_pages pages are left
  * unwritten, and so are those of (sequence, kv head) pairs that need a table entry that is no

@@ -13,8 +13,7 @@
 // A CTA is four warps over one tile: K and V rows arrive by 16-byte cp.async, two or three tiles
 // ahead, in shared memory whose 16-byte chunks are permuted by chunk ^ (row % 8); mma.sync (m16n8k16, BF16 in,
 // FP32 sums) takes K by ldmatrix and V by ldmatrix.trans. With at most 16 query rows each warp takes 16 of the
-// tile's 64 keys and its own m, l and o, joined at the pair's end; with up to 32 two warps share a key half, with
-// up to 64 each warp has 16 rows and all keys. mma.sync is enough: at 16 rows the products need about a sixth of its
+// tile's 64 keys and its own m, l and o, joined at the pair's end; with up to 32 two warps share a key half. mma.sync is enough: at 16 rows the products need about a sixth of its
 // rate while HBM is saturated. p is rounded to BF16 for the second product (half a step, 2^-9 of each weight, below
 // the BF16 output's own rounding); l sums the unrounded p.
 #include <algorithm>
@@ -120,7 +119,7 @@ template <int D, int MT>
 struct DecodeCfg {
     static constexpr int KG = 4 / MT;             // key groups: warps that split a tile's keys
     static constexpr int KPW = kTile / KG;        // keys of a tile per warp
-    static constexpr int STAGES = D == 64 ? 4 : (MT == 4 ? 2 : 3);
+    static constexpr int STAGES = D == 64 ? 4 : 3;
     static constexpr int HALF = kTile * D * 2;    // bytes of a tile's K (or V)
     static constexpr int ROWS = 16 * MT;
     // row stride of the join buffer: eight channels more put the eight rows that a warp writes at once on
@@ -130,7 +129,7 @@ struct DecodeCfg {
     static constexpr int OFF_ML = OFF_O + ROWS * OD * 4;       // [KG][ROWS][2]
     static constexpr int OFF_MISC = OFF_ML + KG * ROWS * 8;    // scan, cursor, flags
     static constexpr int BYTES = OFF_MISC + 256;
-    static constexpr int CTAS = D == 64 ? (MT == 4 ? 2 : 3) : 2;  // resident per SM
+    static constexpr int CTAS = D == 64 ? 3 : 2;  // resident per SM
 };
 
 template <int D, int MT>
@@ -558,8 +557,8 @@ int launch_decode(const DecodeArgs &a, int grid, cudaStream_t s) {
     return launch_after(join_kernel<D>, dim3(grid - 1, a.G * a.K), dim3(32 * kJoinWarps), 0, s, a, grid);
 }
 
-int ctas_per_sm(int D, int mt) { return D == 64 ? (mt == 4 ? 2 : 3) : 2; }
-int m_tiles(int rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 4); }
+int ctas_per_sm(int D) { return D == 64 ? 3 : 2; }
+int m_tiles(int rows) { return rows <= 16 ? 1 : 2; }
 
 size_t info_bytes(int grid) { return (1 + 5 * static_cast<size_t>(grid)) * 8 / 16 * 16 + 16; }
 
@@ -567,7 +566,7 @@ size_t info_bytes(int grid) { return (1 + 5 * static_cast<size_t>(grid)) * 8 / 1
 
 size_t attn_rows_scratch_bytes(int K, int heads, const kda_kv_cache *cache) {
     const size_t rows = static_cast<size_t>(heads / cache->kv_heads) * K;
-    const int grid = ctas_per_sm(cache->head_dim, m_tiles(static_cast<int>(rows))) * num_sms();
+    const int grid = ctas_per_sm(cache->head_dim) * num_sms();
     return info_bytes(grid) + static_cast<size_t>(grid) * 2 * rows * (cache->head_dim + 4) * sizeof(float);
 }
 
@@ -593,16 +592,13 @@ int attn_rows(const kda_kv_cache *cache, int layer, const uint16_t *q, const int
     a.sinks = std::min(sinks, a.c.max_pages * a.c.page_size);
     a.scale2 = dims->scale * kLog2e;
     const int rows = a.G * K, mt = m_tiles(rows), D = dims->head_dim;
-    const int grid = ctas_per_sm(D, mt) * num_sms();
+    const int grid = ctas_per_sm(D) * num_sms();
     char *const p = static_cast<char *>(scratch);
     a.info = reinterpret_cast<long long *>(p);
     a.part_o = reinterpret_cast<float *>(p + info_bytes(grid));
     a.part_ml = a.part_o + static_cast<size_t>(grid) * 2 * rows * D;
-    if (D == 128)
-        return mt == 1 ? launch_decode<128, 1>(a, grid, s)
-                       : (mt == 2 ? launch_decode<128, 2>(a, grid, s) : launch_decode<128, 4>(a, grid, s));
-    return mt == 1 ? launch_decode<64, 1>(a, grid, s)
-                   : (mt == 2 ? launch_decode<64, 2>(a, grid, s) : launch_decode<64, 4>(a, grid, s));
+    if (D == 128) return mt == 1 ? launch_decode<128, 1>(a, grid, s) : launch_decode<128, 2>(a, grid, s);
+    return mt == 1 ? launch_decode<64, 1>(a, grid, s) : launch_decode<64, 2>(a, grid, s);
 }
 
 namespace {
@@ -612,8 +608,9 @@ int check_shape(int N, int K, const kda_dims *dims, const kda_kv_cache *cache) {
     KDA_TRY(check_dims(dims));
     if (N < 0 || K < 0) return KDA_ERR_INVALID_ARG;
     if (dims->head_dim != cache->head_dim || dims->heads % cache->kv_heads) return KDA_ERR_INVALID_ARG;
-    if (static_cast<long long>(dims->heads / cache->kv_heads) * K > kAttnRowsMax) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(dims->heads / cache->kv_heads) * K > 64) return KDA_ERR_UNSUPPORTED;
     if (static_cast<long long>(N) * K > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (!few_rows(K, dims->heads, cache) && !attn_tiles_fits(N, N * K, dims->heads, cache)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
@@ -624,7 +621,8 @@ extern "C" {
 
 size_t kda_attn_decode_scratch_bytes(int N, int K, const kda_dims *dims, const kda_kv_cache *cache) {
     if (kda::check_shape(N, K, dims, cache) != KDA_OK || N == 0 || K == 0) return 0;
-    return kda::attn_rows_scratch_bytes(K, dims->heads, cache);
+    return kda::few_rows(K, dims->heads, cache) ? kda::attn_rows_scratch_bytes(K, dims->heads, cache)
+                                                : kda::attn_tiles_scratch_bytes(N, N * K, dims->heads, cache);
 }
 
 int kda_attn_decode(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *slots, int N, int K, int window,
@@ -634,11 +632,11 @@ int kda_attn_decode(const kda_kv_cache *cache, int layer, const kda_bf16 *q, con
     if (!q || !out || window < 0 || sinks < 0 || layer < 0 || layer >= cache->layers) return KDA_ERR_INVALID_ARG;
     if (!kda::aligned16(q) || !kda::aligned16(out)) return KDA_ERR_MISALIGNED;
     if (N == 0 || K == 0) return KDA_OK;
-    if (!scratch) return KDA_ERR_INVALID_ARG;
-    if (!kda::aligned16(scratch)) return KDA_ERR_MISALIGNED;
-    if (scratch_bytes < kda::attn_rows_scratch_bytes(K, dims->heads, cache)) return KDA_ERR_CAPACITY;
-    return kda::attn_rows(cache, layer, q, nullptr, slots, N, K, N * K, window, sinks, out, lse, scratch, dims,
-                          static_cast<cudaStream_t>(stream));
+    KDA_TRY(kda::check_scratch(scratch, scratch_bytes, kda_attn_decode_scratch_bytes(N, K, dims, cache)));
+    auto s = static_cast<cudaStream_t>(stream);
+    if (kda::few_rows(K, dims->heads, cache))
+        return kda::attn_rows(cache, layer, q, nullptr, slots, N, K, N * K, window, sinks, out, lse, scratch, dims, s);
+    return kda::attn_tiles(cache, layer, q, nullptr, slots, N, K, N * K, window, sinks, out, lse, scratch, dims, s);
 }
 
 }  // extern "C"

@@ -37,7 +37,8 @@ namespace {
 
 using namespace umma;
 
-constexpr int kRows = 256, kKeys = 128, kPrefillThreads = 384;
+constexpr int kKeys = 128;
+constexpr int kSplitTiles = 4;  // the least tiles of a walk's part
 constexpr long long kPrefillWait = 4000000000LL;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.0f;  // log2 of how far a maximum may outgrow its reference
@@ -58,10 +59,16 @@ struct PrefillArgs {
     uint32_t flip;  // sign bits of a BF16 pair if scale < 0 (the queries are negated), else 0
 };
 
+// Rows of a CTA's tile: see the head of the file.
+__host__ __device__ constexpr int halves_of(int D) { return D == 64 ? 1 : 2; }
+__host__ __device__ constexpr int tile_rows(int D) { return 128 * halves_of(D); }
+
 template <int D>
 struct PrefillCfg {
+    static constexpr int NH = halves_of(D), ROWS = tile_rows(D), THREADS = 128 * (NH + 1), CTAS = NH == 1 ? 2 : 1;
+    static constexpr int TMEM = 256 * NH, COL_O = 128 * NH;  // columns: S of the halves, then O of the halves
     static constexpr int TILE = kKeys * D * 2;  // bytes of a Q half, K or V tile
-    static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + 2 * TILE, OFF_BARS = OFF_V + 2 * TILE;
+    static constexpr int OFF_K = NH * TILE, OFF_V = OFF_K + 2 * TILE, OFF_BARS = OFF_V + 2 * TILE;
     static constexpr int BYTES = OFF_BARS + 256 + 1024;
 };
 
@@ -207,15 +214,17 @@ __device__ __forceinline__ bool has_dead_rows(const Tile &t, int i) {
     return i >= t.dead_from || i <= t.dead_to;
 }
 
-// Finds the 256-row tile of `slot` (all threads call; `found` in shared memory): tiles of sequence b start at slot
-// floor(cu[b] G / 256) + b, which keeps them apart whatever the lengths. False: no such tile, or its sequence
+// Finds the row tile of `slot` (all threads call; `found` in shared memory): tiles of sequence b start at slot
+// floor(cu[b] G / ROWS) + b, which keeps them apart whatever the lengths. False: no such tile, or its sequence
 // is refused. `check`: look every sequence over and latch what is wrong.
+__device__ __forceinline__ int row_bound(const PrefillArgs &a, int b) { return a.cu ? a.cu[b] : b * a.max_rows; }
+template <int ROWS>
 __device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, bool check, int *found, Tile &t) {
     if (threadIdx.x == 0) *found = 0x7fffffff;
     __syncthreads();
-    auto first_slot = [&](int b, int c) { return static_cast<long long>(c) * a.G / kRows + b; };
+    auto first_slot = [&](int b, int c) { return static_cast<long long>(c) * a.G / ROWS + b; };
     for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-        const int c0 = a.cu[b], c1 = a.cu[b + 1];
+        const int c0 = row_bound(a, b), c1 = row_bound(a, b + 1);
         if (first_slot(b, c0) <= slot && slot < first_slot(b + 1, c1)) atomicMin(found, b);
         if (check) {
             const int s = a.slots ? a.slots[b] : b;
@@ -227,17 +236,17 @@ __device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, bool chec
     __syncthreads();
     t.b = *found;
     if (t.b >= a.B) return false;
-    t.c0 = a.cu[t.b];
-    const int c1 = a.cu[t.b + 1];
+    t.c0 = row_bound(a, t.b);
+    const int c1 = row_bound(a, t.b + 1);
     t.n = c1 - t.c0;
     t.slot = a.slots ? a.slots[t.b] : t.b;
     if (t.c0 < 0 || c1 < t.c0 || c1 > a.total || t.n > a.max_rows || t.slot < 0 || t.slot >= a.c.max_seqs) return false;
     t.len = a.c.len[t.slot];
     if (t.len < 0 || t.len > a.c.max_pages * a.c.page_size) return false;
-    const long long r0 = (slot - first_slot(t.b, t.c0)) * kRows, all_rows = static_cast<long long>(t.n) * a.G;
+    const long long r0 = (slot - first_slot(t.b, t.c0)) * ROWS, all_rows = static_cast<long long>(t.n) * a.G;
     if (r0 < 0 || r0 >= all_rows) return false;
     t.r0 = static_cast<int>(r0);
-    t.rows = static_cast<int>(min(static_cast<long long>(kRows), all_rows - r0));
+    t.rows = static_cast<int>(min(static_cast<long long>(ROWS), all_rows - r0));
     t.base = t.len - t.n;
     const int p_lo = t.base + t.r0 / a.G;
     t.p_hi_a = t.base + (t.r0 + min(t.rows, 128) - 1) / a.G;
@@ -252,8 +261,13 @@ __device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, bool chec
     return true;
 }
 
+// Into how many parts a tile's walk is cut: short walks are not.
+__device__ __forceinline__ int parts_of(const PrefillArgs &a, const Tile &t) {
+    return min(a.splits, max(1, t.all / kSplitTiles));
+}
+
 template <int D>
-__global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs a) {
+__global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) prefill_kernel(const __grid_constant__ PrefillArgs a) {
     using C = PrefillCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *const sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -268,14 +282,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     volatile int *const bad_page = abort + 1;
     int *const sfound = const_cast<int *>(bad_page + 1);
 
+    constexpr int W = 4 * C::NH;  // the softmax warps come first
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int hk = a.c.kv_heads, split = blockIdx.x % a.splits, h = blockIdx.x / a.splits % hk;
     const int slot_id = a.nslots - 1 - static_cast<int>(blockIdx.x / a.splits / hk);  // the longest walks first
 
     Tile t;
-    if (!locate(a, slot_id, blockIdx.x == 0, sfound, t)) return;
-    t.first = static_cast<int>(static_cast<long long>(t.all) * split / a.splits);
-    const int ntiles = static_cast<int>(static_cast<long long>(t.all) * (split + 1) / a.splits) - t.first;
+    if (!locate<C::ROWS>(a, slot_id, blockIdx.x == 0, sfound, t)) return;
+    const int splits = parts_of(a, t);
+    if (split >= splits) return;
+    t.first = static_cast<int>(static_cast<long long>(t.all) * split / splits);
+    const int ntiles = static_cast<int>(static_cast<long long>(t.all) * (split + 1) / splits) - t.first;
     t.sinks_to = t.sink - t.first;
     t.skip = t.first - t.sink + t.lo / kKeys;
     t.dead_to = t.lo > 0 ? t.sinks_to : -1;
@@ -294,15 +311,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             mbar_init(&fixgo[s], 1);
             mbar_init(&ofull[s], 1);
         }
-        mbar_init(qfull, 8);
+        mbar_init(qfull, W);
         mbar_init(first_k, 1);
         mbar_init(first_read, 1);
         *abort = 0;
         *bad_page = 0;
         fence_mbar_init();
     }
-    if (warp == 9) {
-        tmem_alloc(tmem_slot, 512);
+    if (warp == W + 1) {
+        tmem_alloc(tmem_slot, C::TMEM);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -311,9 +328,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     grid_release();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
-    if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-      if (warp == 8) {
+    if (warp >= W) {
+      if constexpr (C::NH == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if (warp == W) {
         // ---- TMA: lane l brings box l of a tile (page l / (D / 64), 64-channel half l % (D / 64))
         constexpr int HALVES = D / 64;
         const int box_rows = min(a.c.page_size, kKeys), boxes = kKeys / box_rows * HALVES;
@@ -366,7 +384,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             mbar_wait(first_k, 0, 100000000LL);
             for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(&full[i & 1], (i >> 1) & 1, 100000000LL);
         }
-      } else if (warp == 9) {
+      } else if (warp == W + 1) {
         // ---- MMA; what it waits for is nearly always there but P
         if (ntiles > 0) {
             constexpr uint32_t id_s = idesc_bf16(128, kKeys, false, false), id_o = idesc_bf16(128, D, false, true);
@@ -401,7 +419,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             if (ok) {
                 tc_fence_after();
                 if (t.tiles_a > 0) scores(0, 0);
-                if (t.tiles_b > 0) scores(1, 0);
+                if (C::NH == 2 && t.tiles_b > 0) scores(1, 0);
                 commit(first_read);
                 ok = operands(0);
             }
@@ -409,7 +427,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
                 const int s = i & 1;
                 const uint64_t dv = mnmaj_desc(sq + C::OFF_V + s * C::TILE, kKeys, 0, 0);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int x = 0; x < C::NH; ++x) {
                     const int tiles = x ? t.tiles_b : t.tiles_a;
                     if (ok && i < tiles) {
 #pragma unroll
@@ -420,7 +438,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
                             if (elect_one()) {
 #pragma unroll
                                 for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                                    mma_bf16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 8 * ks, dv + mnmaj_step(ks), id_o, i > 0 || ks > 0);
+                                    mma_bf16_ta(tmem + C::COL_O + 128 * x, tmem + 128 * x + 8 * ks, dv + mnmaj_step(ks), id_o, i > 0 || ks > 0);
                             }
                             __syncwarp();
                         }
@@ -435,7 +453,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
                 }
             }
         }
-      } else if (warp == 10) {
+      } else if (warp == W + 2) {
         // ---- V rows that no row of this CTA sees: zeros. fixgo says that the tile's load is under way, so that
         // full's phase is the tile's own (tiles without such rows pass unseen here)
         uint32_t gone = 0;
@@ -457,7 +475,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
         }
       }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (C::NH == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---- softmax: this thread's row of half x
         const int x = warp >> 2, r = 128 * x + 32 * (warp & 3) + lane;
         const bool real = r < t.rows;
@@ -480,7 +499,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
         }
-        const uint32_t ts = tmem_lane_base(tmem, warp) + 128 * x, to = tmem_lane_base(tmem, warp) + 256 + 128 * x;
+        const uint32_t ts = tmem_lane_base(tmem, warp) + 128 * x, to = tmem_lane_base(tmem, warp) + C::COL_O + 128 * x;
         const int p_first = t.base + (t.r0 + 128 * x) / a.G, p_last = x ? t.p_hi_b : t.p_hi_a, tiles = x ? t.tiles_b : t.tiles_a;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
@@ -559,8 +578,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
         }
         if (ok && tiles > 0) ok = wait_or_abort(&ofull[x], 0, abort, a.status);
         tc_fence_after();
-        if (a.splits > 1) {  // this part's l, m and unscaled O; l = -1: a page was none
-            const size_t pr = (static_cast<size_t>(slot_id) * hk + h) * a.splits * kRows + static_cast<size_t>(split) * kRows + r;
+        if (splits > 1) {  // this part's l, m and unscaled O; l = -1: a page was none
+            const size_t pr = (static_cast<size_t>(slot_id) * hk + h) * a.splits * C::ROWS + static_cast<size_t>(split) * C::ROWS + r;
             float4 *const dst = reinterpret_cast<float4 *>(a.part_o + pr * D);
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -601,42 +620,44 @@ __global__ void __launch_bounds__(kPrefillThreads, 1) prefill_kernel(const __gri
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == W + 1) tmem_dealloc(tmem, C::TMEM);
 }
 
 // The parts of split walks, added in order; one warp per row.
 template <int D>
 __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PrefillArgs a) {
-    constexpr int E = D / 32;
+    constexpr int E = D / 32, R = tile_rows(D);
     __shared__ int found;
     grid_acquire();
     const int hk = a.c.kv_heads, h = blockIdx.x % hk, slot = blockIdx.x / hk, lane = threadIdx.x & 31;
     Tile t;
-    if (!locate(a, slot, false, &found, t)) return;
-    const float *const ml = a.part_ml + 2 * (static_cast<size_t>(slot) * hk + h) * a.splits * kRows;
-    const float *const po = a.part_o + (static_cast<size_t>(slot) * hk + h) * a.splits * kRows * D;
+    if (!locate<R>(a, slot, false, &found, t)) return;
+    const int splits = parts_of(a, t);
+    if (splits == 1) return;
+    const float *const ml = a.part_ml + 2 * (static_cast<size_t>(slot) * hk + h) * a.splits * R;
+    const float *const po = a.part_o + (static_cast<size_t>(slot) * hk + h) * a.splits * R * D;
     const int r = 8 * blockIdx.y + (threadIdx.x >> 5);
     if (r >= t.rows) return;
     float m = -INFINITY;
     bool bad = false;
-    for (int p = 0; p < a.splits; ++p) {
-        m = fmaxf(m, ml[2 * (p * kRows + r)]);
-        bad |= ml[2 * (p * kRows + r) + 1] == -1.f;
+    for (int p = 0; p < splits; ++p) {
+        m = fmaxf(m, ml[2 * (p * R + r)]);
+        bad |= ml[2 * (p * R + r) + 1] == -1.f;
     }
     // a page that is none leaves the whole tile, as an unsplit walk does
-    for (int p = 0; p < a.splits; ++p)
-        for (int k = lane; k < t.rows; k += 32) bad |= ml[2 * (p * kRows + k) + 1] == -1.f;
+    for (int p = 0; p < splits; ++p)
+        for (int k = lane; k < t.rows; k += 32) bad |= ml[2 * (p * R + k) + 1] == -1.f;
     if (__any_sync(0xffffffffu, bad)) return;
     float l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
-    for (int p = 0; p < a.splits; ++p) {
-        const float lp = ml[2 * (p * kRows + r) + 1];
+    for (int p = 0; p < splits; ++p) {
+        const float lp = ml[2 * (p * R + r) + 1];
         if (lp == 0.f) continue;  // that part saw nothing and left no O
-        const float w = ex2(ml[2 * (p * kRows + r)] - m);
+        const float w = ex2(ml[2 * (p * R + r)] - m);
         l = fmaf(lp, w, l);
-        const float *const src = po + (static_cast<size_t>(p) * kRows + r) * D + E * lane;
+        const float *const src = po + (static_cast<size_t>(p) * R + r) * D + E * lane;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], w, o[e]);
     }
@@ -652,12 +673,14 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
     if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// CTAs that share the walk of one (256-row tile, kv head): enough that all walks together fill the SMs, at most 16, and
-// none shorter than two tiles of the longest cache. total_tokens G / 256 tiles, or one per sequence, are the fewest there are.
+// CTAs that share the walk of one (row tile, kv head): enough that all walks together fill the SMs, at most 16, and
+// none shorter than kSplitTiles of the longest cache. total G / rows tiles, or one per sequence, are the fewest there are.
 int prefill_splits(int B, int total, int G, const kda_kv_cache *c) {
-    const long long fewest = std::max<long long>(std::min(B, total), (static_cast<long long>(total) * G + kRows - 1) / kRows);
+    const int R = tile_rows(c->head_dim);
+    const long long fewest = std::max<long long>(std::min(B, total), (static_cast<long long>(total) * G + R - 1) / R);
     const long long tiles = (static_cast<long long>(c->max_pages) * c->page_size + kKeys - 1) / kKeys;
-    return static_cast<int>(std::max<long long>(1, std::min<long long>({16, num_sms() / (fewest * c->kv_heads), tiles / 2})));
+    const long long room = static_cast<long long>(num_sms()) * (R == 128 ? 2 : 1);
+    return static_cast<int>(std::max<long long>(1, std::min<long long>({16, room / (fewest * c->kv_heads), tiles / kSplitTiles})));
 }
 
 // 2-D map over a layer's pool as rows of D values; boxes of 64 channels x min(page, 128) rows.
@@ -678,16 +701,68 @@ template <int D>
 int launch_prefill(const PrefillArgs &a, unsigned grid, cudaStream_t s) {
     static std::atomic<unsigned long long> attr{0};
     KDA_TRY(smem_opt_in(prefill_kernel<D>, PrefillCfg<D>::BYTES, attr));
-    prefill_kernel<D><<<grid * a.splits, kPrefillThreads, PrefillCfg<D>::BYTES, s>>>(a);
+    prefill_kernel<D><<<grid * a.splits, PrefillCfg<D>::THREADS, PrefillCfg<D>::BYTES, s>>>(a);
     KDA_TRY(launch_status());
     if (a.splits == 1) return KDA_OK;
-    return launch_after(prefill_join_kernel<D>, dim3(grid, kRows / 8), dim3(256), 0, s, a);
+    return launch_after(prefill_join_kernel<D>, dim3(grid, tile_rows(D) / 8), dim3(256), 0, s, a);
 }
 
 }  // namespace
 }  // namespace kda
 
 namespace kda {
+
+namespace {
+long long tile_slots(int B, int total, int G, int D) { return static_cast<long long>(total) * G / tile_rows(D) + B; }
+}  // namespace
+
+bool attn_tiles_fits(int B, int total, int heads, const kda_kv_cache *cache) {
+    const int G = heads / cache->kv_heads;
+    return static_cast<long long>(total) * G <= 0x7fffffffLL - 256 &&
+           16 * tile_slots(B, total, G, cache->head_dim) * cache->kv_heads <= 0x7fffffffLL;
+}
+
+size_t attn_tiles_scratch_bytes(int B, int total, int heads, const kda_kv_cache *cache) {
+    const int G = heads / cache->kv_heads, splits = prefill_splits(B, total, G, cache);
+    if (splits == 1) return 0;
+    const size_t slots = static_cast<size_t>(tile_slots(B, total, G, cache->head_dim));
+    return slots * cache->kv_heads * splits * tile_rows(cache->head_dim) * (cache->head_dim + 4) * sizeof(float);
+}
+
+int attn_tiles(const kda_kv_cache *cache, int layer, const uint16_t *q, const int *cu, const int *slots, int B,
+               int max_rows, int total, int window, int sinks, uint16_t *out, float *lse, void *scratch,
+               const kda_dims *dims, cudaStream_t s) {
+    PrefillArgs a{};
+    const int D = cache->head_dim;
+    a.G = dims->heads / cache->kv_heads;
+    a.nslots = static_cast<int>(tile_slots(B, total, a.G, D));
+    a.splits = prefill_splits(B, total, a.G, cache);
+    a.status = device_status_ptr();
+    if (!a.status) return KDA_ERR_CUDA;
+    a.c = kv_view(cache, layer);
+    KDA_TRY(make_pool_map(&a.tk, a.c.k, a.c, D));
+    KDA_TRY(make_pool_map(&a.tv, a.c.v, a.c, D));
+    a.q = q;
+    a.cu = cu;
+    a.slots = slots;
+    a.out = out;
+    a.lse = lse;
+    a.B = B;
+    a.max_rows = max_rows;
+    a.total = total;
+    a.heads = dims->heads;
+    // a window that holds the longest sequence is none
+    a.window = window < a.c.max_pages * a.c.page_size ? window : 0;
+    a.sinks = std::min(sinks, a.c.max_pages * a.c.page_size);
+    // a negative scale is taken as negated queries, and 0 as one so small that every weight is 1
+    a.scale2 = std::max(std::fabs(dims->scale) * 1.4426950408889634f, 1e-30f);
+    a.flip = dims->scale < 0.f ? 0x80008000u : 0u;
+    a.part_o = static_cast<float *>(scratch);
+    a.part_ml = a.part_o + static_cast<size_t>(a.nslots) * cache->kv_heads * a.splits * tile_rows(D) * D;
+    const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.nslots) * cache->kv_heads);
+    return D == 128 ? launch_prefill<128>(a, grid, s) : launch_prefill<64>(a, grid, s);
+}
+
 namespace {
 
 int check_prefill(int B, int max_rows, int total, const kda_dims *dims, const kda_kv_cache *cache) {
@@ -696,17 +771,7 @@ int check_prefill(int B, int max_rows, int total, const kda_dims *dims, const kd
     if (B < 0 || max_rows < 0 || total < 0) return KDA_ERR_INVALID_ARG;
     if (dims->head_dim != cache->head_dim || dims->heads % cache->kv_heads) return KDA_ERR_INVALID_ARG;
     if (B > 65535 || dims->heads > 65535) return KDA_ERR_UNSUPPORTED;
-    const int G = dims->heads / cache->kv_heads;
-    const long long slots = static_cast<long long>(total) * G / kRows + B;
-    if (static_cast<long long>(total) * G > 0x7fffffffLL - kRows || slots * cache->kv_heads > 0x7fffffffLL)
-        return KDA_ERR_UNSUPPORTED;
-    return KDA_OK;
-}
-
-// Few rows per sequence go to the split form on mma.sync, whose CTAs share the cache evenly (8 sequences of at most 4 rows
-// over 2000 tokens: see the file's head for both); the rest here.
-bool few_rows(int max_rows, const kda_dims *dims, const kda_kv_cache *cache) {
-    return static_cast<long long>(dims->heads / cache->kv_heads) * max_rows <= kAttnRowsMax;
+    return attn_tiles_fits(B, total, dims->heads, cache) ? KDA_OK : KDA_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -718,11 +783,8 @@ size_t kda_attn_prefill_scratch_bytes(int B, int max_rows, int total_tokens, con
                                       const kda_kv_cache *cache) {
     if (kda::check_prefill(B, max_rows, total_tokens, dims, cache) != KDA_OK || B == 0 || total_tokens == 0 || max_rows == 0)
         return 0;
-    if (kda::few_rows(max_rows, dims, cache)) return kda::attn_rows_scratch_bytes(max_rows, dims->heads, cache);
-    const int G = dims->heads / cache->kv_heads, splits = kda::prefill_splits(B, total_tokens, G, cache);
-    if (splits == 1) return 0;
-    const size_t slots = static_cast<size_t>(total_tokens) * G / kda::kRows + B;
-    return slots * cache->kv_heads * splits * kda::kRows * (cache->head_dim + 4) * sizeof(float);
+    if (kda::few_rows(max_rows, dims->heads, cache)) return kda::attn_rows_scratch_bytes(max_rows, dims->heads, cache);
+    return kda::attn_tiles_scratch_bytes(B, total_tokens, dims->heads, cache);
 }
 
 int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *cu_seqlens, const int *slots,
@@ -735,43 +797,13 @@ int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_bf16 *q, co
     if (B == 0 || total_tokens == 0) return KDA_OK;
     if (max_rows == 0) return KDA_ERR_INVALID_ARG;
     const size_t need = kda_attn_prefill_scratch_bytes(B, max_rows, total_tokens, dims, cache);
-    if (need) {
-        if (!scratch) return KDA_ERR_INVALID_ARG;
-        if (!kda::aligned16(scratch)) return KDA_ERR_MISALIGNED;
-        if (scratch_bytes < need) return KDA_ERR_CAPACITY;
-    }
+    KDA_TRY(kda::check_scratch(scratch, scratch_bytes, need));
     auto s = static_cast<cudaStream_t>(stream);
-    if (kda::few_rows(max_rows, dims, cache))
+    if (kda::few_rows(max_rows, dims->heads, cache))
         return kda::attn_rows(cache, layer, q, cu_seqlens, slots, B, max_rows, total_tokens, window, sinks, out, lse,
                               scratch, dims, s);
-    kda::PrefillArgs a{};
-    a.G = dims->heads / cache->kv_heads;
-    a.nslots = static_cast<int>(static_cast<long long>(total_tokens) * a.G / kda::kRows + B);
-    a.splits = kda::prefill_splits(B, total_tokens, a.G, cache);
-    a.status = kda::device_status_ptr();
-    if (!a.status) return KDA_ERR_CUDA;
-    a.c = kda::kv_view(cache, layer);
-    KDA_TRY(kda::make_pool_map(&a.tk, a.c.k, a.c, cache->head_dim));
-    KDA_TRY(kda::make_pool_map(&a.tv, a.c.v, a.c, cache->head_dim));
-    a.q = q;
-    a.cu = cu_seqlens;
-    a.slots = slots;
-    a.out = out;
-    a.lse = lse;
-    a.B = B;
-    a.max_rows = max_rows;
-    a.total = total_tokens;
-    a.heads = dims->heads;
-    // a window that holds the longest sequence is none
-    a.window = window < a.c.max_pages * a.c.page_size ? window : 0;
-    a.sinks = std::min(sinks, a.c.max_pages * a.c.page_size);
-    // a negative scale is taken as negated queries, and 0 as one so small that every weight is 1
-    a.scale2 = std::max(std::fabs(dims->scale) * 1.4426950408889634f, 1e-30f);
-    a.flip = dims->scale < 0.f ? 0x80008000u : 0u;
-    a.part_o = static_cast<float *>(scratch);
-    a.part_ml = a.part_o + static_cast<size_t>(a.nslots) * cache->kv_heads * a.splits * kda::kRows * cache->head_dim;
-    const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.nslots) * cache->kv_heads);
-    return cache->head_dim == 128 ? kda::launch_prefill<128>(a, grid, s) : kda::launch_prefill<64>(a, grid, s);
+    return kda::attn_tiles(cache, layer, q, cu_seqlens, slots, B, max_rows, total_tokens, window, sinks, out, lse,
+                           scratch, dims, s);
 }
 
 }  // extern "C"

@@ -67,12 +67,31 @@ int launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaS
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-// Attention of a few query rows per sequence, split over the cached rows (kda_attn_decode.cu): K rows of each
-// sequence, or with cu (device, row bounds) at most K. heads / kv_heads * K <= kAttnRowsMax; scratch as sized.
-constexpr int kAttnRowsMax = 64;
+// Attention of a few query rows per sequence, split evenly over the cached rows on mma.sync (kda_attn_decode.cu): K rows
+// of each sequence, or with cu (device, row bounds) at most K; few_rows(K, ..) holds.
 size_t attn_rows_scratch_bytes(int K, int heads, const kda_kv_cache *cache);
 int attn_rows(const kda_kv_cache *cache, int layer, const uint16_t *q, const int *cu, const int *slots, int N, int K,
               int total, int window, int sinks, uint16_t *out, float *lse, void *scratch, const kda_dims *dims,
               cudaStream_t s);
+// The same in tiles of query rows on tcgen05 (kda_attn_prefill.cu): max_rows rows of each sequence, or with cu at most
+// that many. attn_tiles_fits: the tiles' numbers are ints.
+bool attn_tiles_fits(int B, int total, int heads, const kda_kv_cache *cache);
+size_t attn_tiles_scratch_bytes(int B, int total, int heads, const kda_kv_cache *cache);
+int attn_tiles(const kda_kv_cache *cache, int layer, const uint16_t *q, const int *cu, const int *slots, int B,
+               int max_rows, int total, int window, int sinks, uint16_t *out, float *lse, void *scratch,
+               const kda_dims *dims, cudaStream_t s);
+
+// Up to 32 query rows per kv head take the split form, more the tiled one. 64 sequences of 4000 tokens, 8 kv heads
+// of 128, 16 / 32 / 48 / 64 rows: 179 / 222 / 297 / 306 us split, 226 / 226 / 228 / 229 us tiled.
+inline bool few_rows(int rows, int heads, const kda_kv_cache *cache) {
+    return static_cast<long long>(heads / cache->kv_heads) * rows <= 32;
+}
+
+inline int check_scratch(const void *scratch, size_t bytes, size_t need) {
+    if (!need) return KDA_OK;
+    if (!scratch) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(scratch)) return KDA_ERR_MISALIGNED;
+    return bytes < need ? KDA_ERR_CAPACITY : KDA_OK;
+}
 
 }  // namespace kda
