@@ -66,7 +66,11 @@ __host__ __device__ constexpr int tile_rows(int D) { return 128 * halves_of(D); 
 template <int D>
 struct PrefillCfg {
     static constexpr int NH = halves_of(D), ROWS = tile_rows(D), THREADS = 128 * (NH + 1), CTAS = NH == 1 ? 2 : 1;
-    static constexpr int TMEM = 256 * NH, COL_O = 128 * NH;  // columns: S of the halves, then O of the halves
+    // Whether P has TMEM columns of its own: the next S can then be formed as soon as S is in registers
+    static constexpr bool OWN_P = D == 64;
+    // TMEM columns: S of the halves, O of the halves, P (at head_dim 128 P lies over its S)
+    static constexpr int TMEM = 256 * NH, COL_O = 128 * NH, COL_P = OWN_P ? COL_O + D * NH : 0;
+    static constexpr int STEP_P = OWN_P ? 64 : 128;
     static constexpr int TILE = kKeys * D * 2;  // bytes of a Q half, K or V tile
     static constexpr int OFF_K = NH * TILE, OFF_V = OFF_K + 2 * TILE, OFF_BARS = OFF_V + 2 * TILE;
     static constexpr int BYTES = OFF_BARS + 256 + 1024;
@@ -214,35 +218,43 @@ __device__ __forceinline__ bool has_dead_rows(const Tile &t, int i) {
     return i >= t.dead_from || i <= t.dead_to;
 }
 
-// Finds the row tile of `slot` (all threads call; `found` in shared memory): tiles of sequence b start at slot
-// floor(cu[b] G / ROWS) + b, which keeps them apart whatever the lengths. False: no such tile, or its sequence
-// is refused. `check`: look every sequence over and latch what is wrong.
+// Finds the row tile of `slot` (whole warps call): tiles of sequence b start at slot floor(bound(b) G / ROWS) + b, which
+// keeps them apart whatever the lengths; every lane looks at a sequence, so one round of reads does for 32. False:
+// no such tile, or its sequence is refused. `check`: look every sequence over and latch what is wrong.
 __device__ __forceinline__ int row_bound(const PrefillArgs &a, int b) { return a.cu ? a.cu[b] : b * a.max_rows; }
 template <int ROWS>
-__device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, bool check, int *found, Tile &t) {
-    if (threadIdx.x == 0) *found = 0x7fffffff;
-    __syncthreads();
+__device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, bool check, Tile &t) {
     auto first_slot = [&](int b, int c) { return static_cast<long long>(c) * a.G / ROWS + b; };
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-        const int c0 = row_bound(a, b), c1 = row_bound(a, b + 1);
-        if (first_slot(b, c0) <= slot && slot < first_slot(b + 1, c1)) atomicMin(found, b);
-        if (check) {
-            const int s = a.slots ? a.slots[b] : b;
-            bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.total && c1 - c0 <= a.max_rows && s >= 0 && s < a.c.max_seqs;
-            if (ok) ok = a.c.len[s] >= 0 && a.c.len[s] <= a.c.max_pages * a.c.page_size;
-            if (!ok) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+    const int lane = threadIdx.x & 31;
+    t.b = -1;
+    for (int b0 = 0; b0 < a.B && (t.b < 0 || check); b0 += 32) {
+        const int b = b0 + lane;
+        int c0 = 0, c1 = 0, s = -1, len = -1;
+        if (b < a.B) {
+            c0 = row_bound(a, b);
+            c1 = row_bound(a, b + 1);
+            s = a.slots ? a.slots[b] : b;
+            if (s >= 0 && s < a.c.max_seqs) len = a.c.len[s];
+        }
+        const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.total && c1 - c0 <= a.max_rows && len >= 0 &&
+                        len <= a.c.max_pages * a.c.page_size;
+        if (check && b < a.B && !ok) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+        const bool here = b < a.B && first_slot(b, c0) <= slot && slot < first_slot(b + 1, c1);
+        const uint32_t hit = __ballot_sync(0xffffffffu, here);
+        if (hit && t.b < 0) {
+            const int src = __ffs(hit) - 1;
+            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, src)) {
+                t.b = a.B;  // found, and refused
+                continue;
+            }
+            t.b = b0 + src;
+            t.c0 = __shfl_sync(0xffffffffu, c0, src);
+            t.n = __shfl_sync(0xffffffffu, c1, src) - t.c0;
+            t.slot = __shfl_sync(0xffffffffu, s, src);
+            t.len = __shfl_sync(0xffffffffu, len, src);
         }
     }
-    __syncthreads();
-    t.b = *found;
-    if (t.b >= a.B) return false;
-    t.c0 = row_bound(a, t.b);
-    const int c1 = row_bound(a, t.b + 1);
-    t.n = c1 - t.c0;
-    t.slot = a.slots ? a.slots[t.b] : t.b;
-    if (t.c0 < 0 || c1 < t.c0 || c1 > a.total || t.n > a.max_rows || t.slot < 0 || t.slot >= a.c.max_seqs) return false;
-    t.len = a.c.len[t.slot];
-    if (t.len < 0 || t.len > a.c.max_pages * a.c.page_size) return false;
+    if (t.b < 0 || t.b >= a.B) return false;
     const long long r0 = (slot - first_slot(t.b, t.c0)) * ROWS, all_rows = static_cast<long long>(t.n) * a.G;
     if (r0 < 0 || r0 >= all_rows) return false;
     t.r0 = static_cast<int>(r0);
@@ -276,11 +288,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
     uint64_t *const full = reinterpret_cast<uint64_t *>(sm + C::OFF_BARS);
     uint64_t *const empty = full + 2, *const first_k = empty + 2, *const first_read = first_k + 1;
     uint64_t *const sfull = first_read + 1, *const pfull = sfull + 2, *const ofull = pfull + 4, *const vfix = ofull + 2;
-    uint64_t *const fixgo = vfix + 2, *const qfull = fixgo + 2;
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(qfull + 1);
+    uint64_t *const fixgo = vfix + 2, *const qfull = fixgo + 2, *const sfree = qfull + 1;
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(sfree + 2);
     volatile int *const abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *const bad_page = abort + 1;
-    int *const sfound = const_cast<int *>(bad_page + 1);
 
     constexpr int W = 4 * C::NH;  // the softmax warps come first
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -288,7 +299,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
     const int slot_id = a.nslots - 1 - static_cast<int>(blockIdx.x / a.splits / hk);  // the longest walks first
 
     Tile t;
-    if (!locate<C::ROWS>(a, slot_id, blockIdx.x == 0, sfound, t)) return;
+    if (!locate<C::ROWS>(a, slot_id, blockIdx.x == 0 && warp == 0, t)) return;
     const int splits = parts_of(a, t);
     if (split >= splits) return;
     t.first = static_cast<int>(static_cast<long long>(t.all) * split / splits);
@@ -309,6 +320,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             mbar_init(&pfull[2 + s], 4);
             mbar_init(&vfix[s], 1);
             mbar_init(&fixgo[s], 1);
+            mbar_init(&sfree[s], 4);
             mbar_init(&ofull[s], 1);
         }
         mbar_init(qfull, W);
@@ -430,6 +442,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
                 for (int x = 0; x < C::NH; ++x) {
                     const int tiles = x ? t.tiles_b : t.tiles_a;
                     if (ok && i < tiles) {
+                        if (C::OWN_P && i + 1 < tiles) {
+                            if (!(ok = wait_or_abort(&sfree[x], i & 1, abort, a.status))) break;
+                            tc_fence_after();
+                            scores(x, i + 1);
+                        }
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {  // P comes in two halves of 64 keys
                             if (ok) ok = wait_or_abort(&pfull[2 * half + x], i & 1, abort, a.status);
@@ -438,13 +455,13 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
                             if (elect_one()) {
 #pragma unroll
                                 for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                                    mma_bf16_ta(tmem + C::COL_O + 128 * x, tmem + 128 * x + 8 * ks, dv + mnmaj_step(ks), id_o, i > 0 || ks > 0);
+                                    mma_bf16_ta(tmem + C::COL_O + D * x, tmem + C::COL_P + C::STEP_P * x + 8 * ks, dv + mnmaj_step(ks), id_o, i > 0 || ks > 0);
                             }
                             __syncwarp();
                         }
                         if (!ok) break;
-                        if (i + 1 < tiles) scores(x, i + 1);
-                        else commit(&ofull[x]);
+                        if (C::OWN_P || i + 1 == tiles) commit(&ofull[x]);
+                        else scores(x, i + 1);
                     }
                 }
                 if (ok && i + 1 < ntiles) {  // the next operands are looked for while S_b is still running
@@ -499,7 +516,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull);
         }
-        const uint32_t ts = tmem_lane_base(tmem, warp) + 128 * x, to = tmem_lane_base(tmem, warp) + C::COL_O + 128 * x;
+        const uint32_t ts = tmem_lane_base(tmem, warp) + 128 * x, to = tmem_lane_base(tmem, warp) + C::COL_O + D * x;
+        const uint32_t tp = tmem_lane_base(tmem, warp) + C::COL_P + C::STEP_P * x;
         const int p_first = t.base + (t.r0 + 128 * x) / a.G, p_last = x ? t.p_hi_b : t.p_hi_a, tiles = x ? t.tiles_b : t.tiles_a;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
@@ -510,6 +528,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
 #pragma unroll
             for (int c = 0; c < kKeys; c += 32) tmem_ld32(ts + c, s + c);
             tmem_ld_wait();
+            if (C::OWN_P) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfree[x]);
+            }
             const int j0 = tile_row0(t, i);
             if (j0 + kKeys - 1 > p_first || (a.window && j0 <= p_last - a.window)) {
                 // one bit per column: [first, pos] and the sinks, as shifts of ones
@@ -530,6 +553,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             }
             const float mn = max3(max3(top[0], s[kKeys - 4], s[kKeys - 3]), max3(top[1], s[kKeys - 2], s[kKeys - 1]),
                                   fmaxf(top[2], top[3])) * a.scale2;
+            if (C::OWN_P && i > 0) {  // O and the columns of P are the last product's until it is done
+                if (!(ok = wait_or_abort(&ofull[x], (i - 1) & 1, abort, a.status))) break;
+                tc_fence_after();
+            }
             float f = 1.f;
             if (mn > m + kGrow || m == -INFINITY) {  // -inf: the first rows this one sees; its O is still zero
                 const float mx = fmaxf(m, mn);
@@ -564,7 +591,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
                     sum[e & 1] = add2(sum[e & 1], pair(p0, p1));
                     u[e] = pack_bf16(p0, p1);
                 }
-                tmem_st16(ts + c / 2, u);
+                tmem_st16(tp + c / 2, u);
                 if (c == 32 || c == 96) {  // 64 keys' weights are there: their half of the product may start
                     tmem_st_wait();
                     tc_fence_before();
@@ -576,7 +603,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             unpair(add2(sum[0], sum[1]), sum_lo, sum_hi);
             l += sum_lo + sum_hi;
         }
-        if (ok && tiles > 0) ok = wait_or_abort(&ofull[x], 0, abort, a.status);
+        if (ok && tiles > 0) ok = wait_or_abort(&ofull[x], C::OWN_P ? (tiles - 1) & 1 : 0, abort, a.status);
         tc_fence_after();
         if (splits > 1) {  // this part's l, m and unscaled O; l = -1: a page was none
             const size_t pr = (static_cast<size_t>(slot_id) * hk + h) * a.splits * C::ROWS + static_cast<size_t>(split) * C::ROWS + r;
@@ -627,11 +654,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
 template <int D>
 __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PrefillArgs a) {
     constexpr int E = D / 32, R = tile_rows(D);
-    __shared__ int found;
     grid_acquire();
     const int hk = a.c.kv_heads, h = blockIdx.x % hk, slot = blockIdx.x / hk, lane = threadIdx.x & 31;
     Tile t;
-    if (!locate<R>(a, slot, false, &found, t)) return;
+    if (!locate<R>(a, slot, false, t)) return;
     const int splits = parts_of(a, t);
     if (splits == 1) return;
     const float *const ml = a.part_ml + 2 * (static_cast<size_t>(slot) * hk + h) * a.splits * R;
