@@ -153,11 +153,19 @@ def _p(t):
     return t.data_ptr()
 
 
+_raw_stream = None  # torch's handle of a device's current stream, without a Stream object (3 us a call less)
+
+
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
+    global _raw_stream
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        torch.cuda.init()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _call(name: str, *args) -> int:
@@ -581,6 +589,8 @@ class KVCache:
         self.struct = KdaKvCache(_p(k), _p(v), _p(page_table), _p(seq_len), _p(ref), _p(self.scratch),
                                  k.stride(0) if layers > 1 else k[0].numel() if layers else 0, layers, num_pages,
                                  page_size, kv_heads, head_dim, max_seqs, max_pages)
+        self._ref = ctypes.byref(self.struct)
+        self._need = {}  # scratch bytes of the attention calls by their sizes
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, max_seqs: int, max_pages: int,
@@ -595,24 +605,32 @@ class KVCache:
                    torch.zeros(num_pages, dtype=torch.int32, device=device))
 
 
+def _cache(cache: KVCache):
+    """The cache's struct, for a call on its own device."""
+    import torch
+    if cache.k.device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {cache.k.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return cache._ref
+
+
 def kda_kv_reserve(cache: KVCache, slots, add, n: int, stream=None):
     """Room for add[i] more tokens in slot slots[i] (device int32 [n]; slots None: slot i)."""
-    return _call("kda_kv_reserve", ctypes.byref(cache.struct), _p(slots), _p(add), n, _stream(stream))
+    return _call("kda_kv_reserve", _cache(cache), _p(slots), _p(add), n, _stream(stream))
 
 
 def kda_kv_fork(cache: KVCache, parent, child, n: int, stream=None):
     """Slot child[i] becomes a copy of slot parent[i]: full pages shared, a partly filled last page copied."""
-    return _call("kda_kv_fork", ctypes.byref(cache.struct), _p(parent), _p(child), n, _stream(stream))
+    return _call("kda_kv_fork", _cache(cache), _p(parent), _p(child), n, _stream(stream))
 
 
 def kda_kv_truncate(cache: KVCache, slots, new_len, n: int, stream=None):
     """Slot slots[i] keeps its first new_len[i] tokens (0 frees it)."""
-    return _call("kda_kv_truncate", ctypes.byref(cache.struct), _p(slots), _p(new_len), n, _stream(stream))
+    return _call("kda_kv_truncate", _cache(cache), _p(slots), _p(new_len), n, _stream(stream))
 
 
 def kda_kv_compact(cache: KVCache, live=None, stream=None):
     """Move the live pages to the front of the pools; live (device int32 [1]) receives their number."""
-    return _call("kda_kv_compact", ctypes.byref(cache.struct), _p(live), _stream(stream))
+    return _call("kda_kv_compact", _cache(cache), _p(live), _stream(stream))
 
 
 def _rows_stride(name, k_new, v_new) -> int:
@@ -628,7 +646,7 @@ def kda_kv_append(cache: KVCache, layer: int, k_new, v_new, cu_seqlens, slots, B
                   stream=None):
     """Packed new K and V rows ([total_tokens, kv_heads * head_dim] or [total_tokens, kv_heads, head_dim], any row
     stride) into the pages of their sequences, whose last tokens they are."""
-    return _call("kda_kv_append", ctypes.byref(cache.struct), layer, _p(k_new), _p(v_new),
+    return _call("kda_kv_append", _cache(cache), layer, _p(k_new), _p(v_new),
                  _rows_stride("kda_kv_append", k_new, v_new), _p(cu_seqlens), _p(slots), B, total_tokens,
                  _stream(stream))
 
@@ -642,10 +660,13 @@ def kda_attn_prefill_scratch_bytes(B: int, max_rows: int, total_tokens: int, d: 
                                                     ctypes.byref(cache.struct)))
 
 
-def _attn_scratch(need: int, cache: KVCache, stream_handle: int):
-    """The stream's cached buffer; while the current stream is being captured a buffer of the graph's own, so
-    that graphs captured one after the other may run at once."""
+def _attn_scratch(fn, key, d: KdaDims, cache: KVCache, stream_handle: int):
+    """The stream's cached buffer, of at least fn(*key) bytes; while the current stream is being captured a buffer of the
+    graph's own, so that graphs captured one after the other may run at once."""
     import torch
+    need = cache._need.get((key, d.heads, d.head_dim))
+    if need is None:
+        need = cache._need[key, d.heads, d.head_dim] = fn(*key, d, cache)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.k.device)
     return scratch_buffer(need, cache.k.device, stream_handle)
@@ -657,8 +678,8 @@ def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d
     lse [N*K, heads] F32 or None). `scratch`: kda_attn_decode_scratch_bytes bytes; a cached buffer when None."""
     st = _stream(stream)
     if scratch is None:
-        scratch = _attn_scratch(kda_attn_decode_scratch_bytes(N, K, d, cache), cache, st)
-    return _call("kda_attn_decode", ctypes.byref(cache.struct), layer, _p(q), _p(slots), N, K, window, sinks, _p(out),
+        scratch = _attn_scratch(kda_attn_decode_scratch_bytes, (N, K), d, cache, st)
+    return _call("kda_attn_decode", _cache(cache), layer, _p(q), _p(slots), N, K, window, sinks, _p(out),
                  _p(lse), _p(scratch), scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
 
 
@@ -669,7 +690,7 @@ def kda_attn_prefill(cache: KVCache, layer: int, q, cu_seqlens, slots, B: int, m
     kda_attn_decode (kda_attn_prefill_scratch_bytes)."""
     st = _stream(stream)
     if scratch is None:
-        scratch = _attn_scratch(kda_attn_prefill_scratch_bytes(B, max_rows, total_tokens, d, cache), cache, st)
-    return _call("kda_attn_prefill", ctypes.byref(cache.struct), layer, _p(q), _p(cu_seqlens), _p(slots), B, max_rows,
+        scratch = _attn_scratch(kda_attn_prefill_scratch_bytes, (B, max_rows, total_tokens), d, cache, st)
+    return _call("kda_attn_prefill", _cache(cache), layer, _p(q), _p(cu_seqlens), _p(slots), B, max_rows,
                  total_tokens, window, sinks, _p(out), _p(lse), _p(scratch),
                  scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
