@@ -483,33 +483,21 @@ constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ DecodeArgs a, int grid_ctas) {
     constexpr int E = D / 32;
-    __shared__ float so[kJoinWarps][D], ss[kJoinWarps];
-    grid_acquire();
-    const long long all = a.info[0];
-    const int ctas = static_cast<int>(min(static_cast<long long>(grid_ctas), all));
+    __shared__ float so[kJoinWarps][D];
+    __shared__ float2 sml[kJoinWarps];
     const int c = blockIdx.x + 1, r = blockIdx.y, rows = a.G * a.K, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (c >= ctas) return;
     const long long *const f = a.info + 1 + 5LL * c;
-    const long long first = f[1], tiles = f[2];
-    if (r >= a.G * f[4] || run_start(all, ctas, c) == first) return;
+    grid_acquire();
+    const long long all = a.info[0], h = f[0], first = f[1], tiles = f[2], row0 = f[3], n = f[4];  // one round of reads
+    const int ctas = static_cast<int>(min(static_cast<long long>(grid_ctas), all));
+    if (c >= ctas || r >= a.G * n || run_start(all, ctas, c) == first) return;
     const long long before = run_start(all, ctas, c - 1);
     if (before > first) return;
     const int last = run_of(all, ctas, first + tiles - 1), slot0 = before == first ? 0 : 1;
     auto at = [&](int k) { return (static_cast<size_t>(k) * 2 + (k == c - 1 ? slot0 : 0)) * rows + r; };
 
-    // the largest m of the parts, and whether one of them met a bad page
-    float top = -INFINITY;
-    bool bad = false;
-    for (int k = c - 1 + lane; k <= last; k += 32) {
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at(k));
-        top = fmaxf(top, ml.x);
-        bad |= ml.y == -1.f;
-    }
-    if (__any_sync(0xffffffffu, bad)) return;  // the same in every warp
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, v[E];
+    float m = -INFINITY, l = 0.f, v[E];
+    bool bad = false;  // a part met a page that is none
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll 4
@@ -524,24 +512,31 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
             const float2 q = *reinterpret_cast<const float2 *>(src);
             x[0] = q.x, x[1] = q.y;
         }
-        const float w = ex2(ml.x - ref);
-        sum = fmaf(ml.y, w, sum);
+        bad |= ml.y == -1.f;
+        const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn, w0 = ex2(m - ref), w1 = ex2(ml.x - ref);
+        m = mn;
+        l = fmaf(l, w0, ml.y * w1);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = fmaf(x[e], w, v[e]);
+        for (int e = 0; e < E; ++e) v[e] = fmaf(v[e], w0, x[e] * w1);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) so[warp][E * lane + e] = v[e];
-    if (lane == 0) ss[warp] = sum;
-    __syncthreads();
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    if (__syncthreads_or(bad)) return;
     if (threadIdx.x >= D) return;  // D <= 32 kJoinWarps
-    float o = 0.f, l = 0.f;
+    float top = -INFINITY, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sml[w].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    l = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-        o += so[w][threadIdx.x];
-        l += ss[w];
+        const float f1 = ex2(sml[w].x - ref);
+        o = fmaf(so[w][threadIdx.x], f1, o);
+        l = fmaf(sml[w].y, f1, l);
     }
     const int tk = r / a.G;
-    const size_t row = static_cast<size_t>(f[3] + tk) * a.heads + f[0] * a.G + (r - tk * a.G);
+    const size_t row = static_cast<size_t>(row0 + tk) * a.heads + h * a.G + (r - tk * a.G);
     a.out[row * D + threadIdx.x] = f32_to_bf16(l == 0.f ? 0.f : o / l);
     if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
