@@ -14,8 +14,9 @@
 // ahead, in shared memory whose 16-byte chunks are permuted by chunk ^ (row % 8); mma.sync (m16n8k16, BF16 in,
 // FP32 sums) takes K by ldmatrix and V by ldmatrix.trans. With at most 16 query rows each warp takes 16 of the
 // tile's 64 keys and its own m, l and o, joined at the pair's end; with up to 32 two warps share a key half. mma.sync is enough: at 16 rows the products need about a sixth of its
-// rate while HBM is saturated. p is rounded to BF16 for the second product (half a step, 2^-9 of each weight, below
-// the BF16 output's own rounding); l sums the unrounded p.
+// rate while HBM is saturated. p is rounded to BF16 for the second product (at most 2^-9 of each weight); the sum that o is
+// divided by is that of the rounded p (one more product, with ones), so that the roundings cancel where few keys
+// carry a row, and the one that lse takes is that of the unrounded p.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -34,7 +35,7 @@ struct DecodeArgs {
     const int *slots;
     uint16_t *out;
     float *lse;
-    float *part_o, *part_ml;  // [CTA][2][rows][D], [CTA][2][rows][2]
+    float *part_o, *part_ml;  // [CTA][2][rows][D], [CTA][2][rows][4]: m, l (-1: bad page), l of the rounded p
     long long *info;          // [0] all tiles; then per CTA, of the pair that its run starts in: kv head, first tile in the
                               // list, tiles, first query row, query rows
     int *status;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     const int mt = warp % MT, kg = warp / MT;
     const int ra = 16 * mt + (lane >> 2), rb = ra + 8;  // this thread's two rows
     uint32_t qf[D / 16][4];
-    float o[D / 8][4], m[2], l[2];
+    float o[D / 8][4], m[2], l[2], lp[4];  // lp: sums of the rounded p (0, 2: this thread's rows)
     int pos[2];
     bool seg_bad = false;
     // the rows' queries and positions; called before the last pair's results are written, so that the loads run under that
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     auto begin_pair = [&]() {
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
+        lp[0] = lp[1] = lp[2] = lp[3] = 0.f;
 #pragma unroll
         for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
         seg_bad = false;
@@ -364,6 +366,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
             const float f = ex2(m[e] - safe[e]);
             m[e] = mn;
             l[e] *= f;
+            lp[2 * e] *= f;
+            lp[2 * e + 1] *= f;
 #pragma unroll
             for (int d = 0; d < D / 8; ++d) {
                 o[d][2 * e] *= f;
@@ -383,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
             const uint32_t p[4] = {pack_bf16(s[2 * kb][0], s[2 * kb][1]), pack_bf16(s[2 * kb][2], s[2 * kb][3]),
                                    pack_bf16(s[2 * kb + 1][0], s[2 * kb + 1][1]),
                                    pack_bf16(s[2 * kb + 1][2], s[2 * kb + 1][3])};
+            mma16816(lp, p, 0x3f803f80u, 0x3f803f80u);  // p times ones
             const int r = C::KPW * kg + 16 * kb + (lane & 15);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
@@ -434,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
                         for (int d = 0; d < D / 8; ++d)
                             *reinterpret_cast<float2 *>(w + 8 * d) =
                                 make_float2(fmaf(o[d][2 * e], f[e], u[d].x), fmaf(o[d][2 * e + 1], f[e], u[d].y));
+                        if ((lane & 3) == 0) w[D] = fmaf(lp[2 * e], f[e], g ? w[D] : 0.f);  // in the row's padding
                     }
                 }
                 __syncthreads();
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
                     if (!seg_bad) {
                         const int tk = r / a.G;
                         const size_t row = static_cast<size_t>(row0 + tk) * a.heads + h * a.G + (r - tk * a.G);
-                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        const float inv = sum == 0.f ? 0.f : 1.f / so[r * C::OD + D];
                         *reinterpret_cast<uint2 *>(a.out + row * D + d) =
                             make_uint2(pack_bf16(v0.x * inv, v0.y * inv), pack_bf16(v1.x * inv, v1.y * inv));
                         if (a.lse && d == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top_all + log2f(sum)) * kLn2;
@@ -464,7 +470,9 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
                 } else {
                     const size_t pr = (static_cast<size_t>(cta) * 2 + slot) * part_rows + r;
                     *reinterpret_cast<float4 *>(a.part_o + pr * D + d) = make_float4(v0.x, v0.y, v1.x, v1.y);
-                    if (d == 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * pr) = make_float2(top_all, seg_bad ? -1.f : sum);
+                    if (d == 0)
+                        *reinterpret_cast<float4 *>(a.part_ml + 4 * pr) =
+                            make_float4(top_all, seg_bad ? -1.f : sum, so[r * C::OD + D], 0.f);
                 }
             }
             if (seg_bad && tid == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
@@ -484,7 +492,7 @@ template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ DecodeArgs a, int grid_ctas) {
     constexpr int E = D / 32;
     __shared__ float so[kJoinWarps][D];
-    __shared__ float2 sml[kJoinWarps];
+    __shared__ float3 sml[kJoinWarps];
     const int c = blockIdx.x + 1, r = blockIdx.y, rows = a.G * a.K, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long *const f = a.info + 1 + 5LL * c;
     grid_acquire();
@@ -496,13 +504,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     const int last = run_of(all, ctas, first + tiles - 1), slot0 = before == first ? 0 : 1;
     auto at = [&](int k) { return (static_cast<size_t>(k) * 2 + (k == c - 1 ? slot0 : 0)) * rows + r; };
 
-    float m = -INFINITY, l = 0.f, v[E];
+    float m = -INFINITY, l = 0.f, lp = 0.f, v[E];
     bool bad = false;  // a part met a page that is none
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll 4
     for (int k = c - 1 + warp; k <= last; k += kJoinWarps) {
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * at(k));
+        const float4 ml = *reinterpret_cast<const float4 *>(a.part_ml + 4 * at(k));
         const float *const src = a.part_o + at(k) * D + E * lane;
         float x[E];
         if constexpr (E == 4) {
@@ -516,28 +524,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
         const float mn = fmaxf(m, ml.x), ref = mn == -INFINITY ? 0.f : mn, w0 = ex2(m - ref), w1 = ex2(ml.x - ref);
         m = mn;
         l = fmaf(l, w0, ml.y * w1);
+        lp = fmaf(lp, w0, ml.z * w1);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = fmaf(v[e], w0, x[e] * w1);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) so[warp][E * lane + e] = v[e];
-    if (lane == 0) sml[warp] = make_float2(m, l);
+    if (lane == 0) sml[warp] = make_float3(m, l, lp);
     if (__syncthreads_or(bad)) return;
     if (threadIdx.x >= D) return;  // D <= 32 kJoinWarps
     float top = -INFINITY, o = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sml[w].x);
     const float ref = top == -INFINITY ? 0.f : top;
-    l = 0.f;
+    l = lp = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
         const float f1 = ex2(sml[w].x - ref);
         o = fmaf(so[w][threadIdx.x], f1, o);
         l = fmaf(sml[w].y, f1, l);
+        lp = fmaf(sml[w].z, f1, lp);
     }
     const int tk = r / a.G;
     const size_t row = static_cast<size_t>(row0 + tk) * a.heads + h * a.G + (r - tk * a.G);
-    a.out[row * D + threadIdx.x] = f32_to_bf16(l == 0.f ? 0.f : o / l);
+    a.out[row * D + threadIdx.x] = f32_to_bf16(l == 0.f ? 0.f : o / lp);
     if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
