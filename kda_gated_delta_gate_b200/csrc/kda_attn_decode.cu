@@ -123,12 +123,9 @@ struct DecodeCfg {
     static constexpr int STAGES = D == 64 ? 4 : 3;
     static constexpr int HALF = kTile * D * 2;    // bytes of a tile's K (or V)
     static constexpr int ROWS = 16 * MT;
-    // row stride of the join buffer: eight channels more put the eight rows that a warp writes at once on
-    // different banks; two CTAs of 32 rows just fit an SM with two more
-    static constexpr int OD = D + (MT == 2 ? 2 : 8);
-    static constexpr int OFF_O = STAGES * 2 * HALF;            // [ROWS][OD] FP32
-    static constexpr int OFF_ML = OFF_O + ROWS * OD * 4;       // [KG][ROWS][2]
-    static constexpr int OFF_MISC = OFF_ML + KG * ROWS * 8;    // scan, cursor, flags
+    static constexpr int OFF_ML = STAGES * 2 * HALF;           // [KG][ROWS] of (m, l, l of the rounded p, -)
+    static constexpr int OFF_MISC = OFF_ML + KG * ROWS * 16;   // scan, cursor, flags
+    static_assert(KG * ROWS * D * 4 == 2 * HALF, "the warps' o fill the stage of the tile just used");
     static constexpr int BYTES = OFF_MISC + 256;
     static constexpr int CTAS = D == 64 ? 3 : 2;  // resident per SM
 };
@@ -137,8 +134,7 @@ template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using C = DecodeCfg<D, MT>;
     extern __shared__ __align__(128) uint8_t sm[];
-    float *const so = reinterpret_cast<float *>(sm + C::OFF_O);
-    float2 *const sml = reinterpret_cast<float2 *>(sm + C::OFF_ML);
+    float4 *const sml = reinterpret_cast<float4 *>(sm + C::OFF_ML);
     long long *const sscan = reinterpret_cast<long long *>(sm + C::OFF_MISC);  // 4 warp sums
     long long *const scur = sscan + 4;                                         // sequence, its first tile
     int *const sbad = reinterpret_cast<int *>(scur + 2);                       // per stage: a needed entry is no page
@@ -407,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
                 mma16816(o[2 * d + 1], p, b[2], b[3]);
             }
         }
+        float *const so = reinterpret_cast<float *>(sm + stage * 2 * C::HALF);  // free once all warps are here
         if (++stage == C::STAGES) stage = 0;
 
         // ---- the pair's last tile of this run: join the warps, then write the result or this run's part
@@ -423,69 +420,61 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
             for (int e = 0; e < 2; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-                if ((lane & 3) == 0) sml[kg * C::ROWS + (e ? rb : ra)] = make_float2(m[e], l[e]);
+                if ((lane & 3) == 0) sml[kg * C::ROWS + (e ? rb : ra)] = make_float4(m[e], l[e], lp[2 * e], 0.f);
             }
             __syncthreads();
-            float f[2];
+            // every warp's o, [KG][ROWS][D], groups of eight channels permuted by row so that the rows that a warp writes at
+            // once spread over the banks
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float top_all = -INFINITY;
+                const int r = e ? rb : ra;
+                if (r < rows) {
+                    float *const w = so + (kg * C::ROWS + r) * D + 2 * (lane & 3);
 #pragma unroll
-                for (int g = 0; g < C::KG; ++g) top_all = fmaxf(top_all, sml[g * C::ROWS + (e ? rb : ra)].x);
-                f[e] = ex2(m[e] - (top_all == -INFINITY ? 0.f : top_all));
-            }
-#pragma unroll
-            for (int g = 0; g < C::KG; ++g) {  // in key order; a warp's loads all go out before its stores
-                if (kg == g) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float *const w = so + (e ? rb : ra) * C::OD + 2 * (lane & 3);
-                        float2 u[D / 8];
-#pragma unroll
-                        for (int d = 0; d < D / 8; ++d)
-                            u[d] = g ? *reinterpret_cast<const float2 *>(w + 8 * d) : make_float2(0.f, 0.f);
-#pragma unroll
-                        for (int d = 0; d < D / 8; ++d)
-                            *reinterpret_cast<float2 *>(w + 8 * d) =
-                                make_float2(fmaf(o[d][2 * e], f[e], u[d].x), fmaf(o[d][2 * e + 1], f[e], u[d].y));
-                        if ((lane & 3) == 0) w[D] = fmaf(lp[2 * e], f[e], g ? w[D] : 0.f);  // in the row's padding
-                    }
+                    for (int d = 0; d < D / 8; ++d)
+                        *reinterpret_cast<float2 *>(w + 8 * (d ^ (r & 3))) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
                 }
-                __syncthreads();
             }
+            __syncthreads();
             for (int i = tid; i < rows * (D / 4); i += kThreads) {
                 const int r = i / (D / 4), d = 4 * (i % (D / 4));
-                float top_all = -INFINITY, sum = 0.f;
-                float2 ml[C::KG];
+                float top_all = -INFINITY, sum = 0.f, sum_p = 0.f;
+                float4 ml[C::KG], v = make_float4(0.f, 0.f, 0.f, 0.f), u[C::KG];
 #pragma unroll
                 for (int g = 0; g < C::KG; ++g) {
                     ml[g] = sml[g * C::ROWS + r];
+                    u[g] = *reinterpret_cast<const float4 *>(so + (g * C::ROWS + r) * D + (d ^ ((r & 3) << 3)));
                     top_all = fmaxf(top_all, ml[g].x);
                 }
                 const float ref = top_all == -INFINITY ? 0.f : top_all;
 #pragma unroll
-                for (int g = 0; g < C::KG; ++g) sum += ml[g].y * ex2(ml[g].x - ref);
-                const float *const sv = so + r * C::OD + d;
-                const float2 v0 = *reinterpret_cast<const float2 *>(sv), v1 = *reinterpret_cast<const float2 *>(sv + 2);
+                for (int g = 0; g < C::KG; ++g) {  // in key order
+                    const float f = ex2(ml[g].x - ref);
+                    sum = fmaf(ml[g].y, f, sum);
+                    sum_p = fmaf(ml[g].z, f, sum_p);
+                    v.x = fmaf(u[g].x, f, v.x);
+                    v.y = fmaf(u[g].y, f, v.y);
+                    v.z = fmaf(u[g].z, f, v.z);
+                    v.w = fmaf(u[g].w, f, v.w);
+                }
                 if (whole) {
                     if (!seg_bad) {
                         const int tk = r / a.G;
                         const size_t row = static_cast<size_t>(row0 + tk) * a.heads + h * a.G + (r - tk * a.G);
-                        const float inv = sum == 0.f ? 0.f : 1.f / so[r * C::OD + D];
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum_p;
                         *reinterpret_cast<uint2 *>(a.out + row * D + d) =
-                            make_uint2(pack_bf16(v0.x * inv, v0.y * inv), pack_bf16(v1.x * inv, v1.y * inv));
+                            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
                         if (a.lse && d == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top_all + log2f(sum)) * kLn2;
                     }
                 } else {
                     const size_t pr = (static_cast<size_t>(cta) * 2 + slot) * part_rows + r;
-                    *reinterpret_cast<float4 *>(a.part_o + pr * D + d) = make_float4(v0.x, v0.y, v1.x, v1.y);
+                    *reinterpret_cast<float4 *>(a.part_o + pr * D + d) = v;
                     if (d == 0)
-                        *reinterpret_cast<float4 *>(a.part_ml + 4 * pr) =
-                            make_float4(top_all, seg_bad ? -1.f : sum, so[r * C::OD + D], 0.f);
+                        *reinterpret_cast<float4 *>(a.part_ml + 4 * pr) = make_float4(top_all, seg_bad ? -1.f : sum, sum_p, 0.f);
                 }
             }
             if (seg_bad && tid == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
-            __syncthreads();  // so and sml are read; the next pair may overwrite them
+            // the next tile's barrier comes before anything goes into so or sml again
             begin_pair();
         } else {
             ++cc.i;
