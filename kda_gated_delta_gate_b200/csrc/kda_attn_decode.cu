@@ -483,15 +483,17 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Block (c - 1, r): row r of the pair that the cut between runs c - 1 and c splits, if it is the pair's first
-// cut. Four warps take every fourth part each and their sums are added in warp order.
+// The pair that the cut between runs c - 1 and c splits, if that is the pair's first cut: the parts of its rows, added
+// in a fixed order. WIDE: block (c - 1, r) takes row r, every warp every fourth part (a few pairs in many
+// parts); else a warp takes a row and all its parts (many pairs in two or three, and four times fewer blocks).
 constexpr int kJoinWarps = 4;
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ DecodeArgs a, int grid_ctas) {
-    constexpr int E = D / 32;
-    __shared__ float so[kJoinWarps][D];
+    constexpr int E = D / 32, STEP = WIDE ? kJoinWarps : 1;
+    __shared__ float so[kJoinWarps][WIDE ? D : 1];
     __shared__ float3 sml[kJoinWarps];
-    const int c = blockIdx.x + 1, r = blockIdx.y, rows = a.G * a.K, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = a.G * a.K;
+    const int c = blockIdx.x + 1, r = WIDE ? blockIdx.y : kJoinWarps * blockIdx.y + warp;
     const long long *const f = a.info + 1 + 5LL * c;
     grid_acquire();
     const long long all = a.info[0], h = f[0], first = f[1], tiles = f[2], row0 = f[3], n = f[4];  // one round of reads
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll 4
-    for (int k = c - 1 + warp; k <= last; k += kJoinWarps) {
+    for (int k = c - 1 + (WIDE ? warp : 0); k <= last; k += STEP) {
         const float4 ml = *reinterpret_cast<const float4 *>(a.part_ml + 4 * at(k));
         const float *const src = a.part_o + at(k) * D + E * lane;
         float x[E];
@@ -526,27 +528,39 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = fmaf(v[e], w0, x[e] * w1);
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][E * lane + e] = v[e];
-    if (lane == 0) sml[warp] = make_float3(m, l, lp);
-    if (__syncthreads_or(bad)) return;
-    if (threadIdx.x >= D) return;  // D <= 32 kJoinWarps
-    float top = -INFINITY, o = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sml[w].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    l = lp = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        const float f1 = ex2(sml[w].x - ref);
-        o = fmaf(so[w][threadIdx.x], f1, o);
-        l = fmaf(sml[w].y, f1, l);
-        lp = fmaf(sml[w].z, f1, lp);
-    }
     const int tk = r / a.G;
     const size_t row = static_cast<size_t>(row0 + tk) * a.heads + h * a.G + (r - tk * a.G);
-    a.out[row * D + threadIdx.x] = f32_to_bf16(l == 0.f ? 0.f : o / lp);
-    if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+    if constexpr (!WIDE) {
+        if (bad) return;
+        const float inv = l == 0.f ? 0.f : 1.f / lp;
+        uint32_t u[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) u[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
+        uint16_t *const dst = a.out + row * D + E * lane;
+        if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(u[0], u[1]);
+        else *reinterpret_cast<uint32_t *>(dst) = u[0];
+        if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) so[warp][E * lane + e] = v[e];
+        if (lane == 0) sml[warp] = make_float3(m, l, lp);
+        if (__syncthreads_or(bad)) return;
+        if (threadIdx.x >= D) return;  // D <= 32 kJoinWarps
+        float top = -INFINITY, o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sml[w].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        l = lp = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f1 = ex2(sml[w].x - ref);
+            o = fmaf(so[w][threadIdx.x], f1, o);
+            l = fmaf(sml[w].y, f1, l);
+            lp = fmaf(sml[w].z, f1, lp);
+        }
+        a.out[row * D + threadIdx.x] = f32_to_bf16(l == 0.f ? 0.f : o / lp);
+        if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+    }
 }
 
 template <int D, int MT>
@@ -557,7 +571,11 @@ int launch_decode(const DecodeArgs &a, int grid, cudaStream_t s) {
     decode_kernel<D, MT><<<grid, kThreads, C::BYTES, s>>>(a);
     KDA_TRY(launch_status());
     if (grid < 2) return KDA_OK;
-    return launch_after(join_kernel<D>, dim3(grid - 1, a.G * a.K), dim3(32 * kJoinWarps), 0, s, a, grid);
+    const int rows = a.G * a.K;
+    if (static_cast<long long>(a.N) * a.c.kv_heads * 8 < grid)
+        return launch_after(join_kernel<D, true>, dim3(grid - 1, rows), dim3(32 * kJoinWarps), 0, s, a, grid);
+    return launch_after(join_kernel<D, false>, dim3(grid - 1, (rows + kJoinWarps - 1) / kJoinWarps), dim3(32 * kJoinWarps), 0,
+                        s, a, grid);
 }
 
 int ctas_per_sm(int D) { return D == 64 ? 3 : 2; }

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kBookThreads) take_pages_kernel(const KvView c
     __shared__ int sh[32], bad, copies;
     grid_release();
     const BookScratch b = book_scratch(scratch, c.num_pages, c.max_seqs);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     int *const taken = b.map;
     if (tid == 0) bad = 0, copies = 0;
     if (slots) {  // of several listings of a slot the first counts
@@ -180,8 +180,12 @@ __global__ void __launch_bounds__(kBookThreads) take_pages_kernel(const KvView c
         have = visit_pages<true>(c.ref, 0, c.num_pages, static_cast<int>(min(base, static_cast<long long>(c.num_pages))),
                                  sh, [&](int page, int rank) { taken[rank] = page; });
 
-    // one warp per pair; refs and lengths have all been read by now
-    for (int i = warp; i < n; i += kBookThreads / 32) {
+    // `wide` threads per pair, so that few pairs of many pages and many pairs of few both take few rounds; refs and
+    // lengths have all been read by now
+    int wide = kBookThreads;
+    while (wide > 4 && wide * n > kBookThreads) wide >>= 1;
+    const int lane = tid & (wide - 1);
+    for (int i = tid / wide; i < n; i += kBookThreads / wide) {
         int first = b.first[i];
         if (first < 0) continue;
         const int s = slots ? slots[i] : i, len = b.len[i];
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kBookThreads) take_pages_kernel(const KvView c
         }
         const int *const prow = FORK ? c.table + static_cast<size_t>(from[i]) * c.max_pages : row;
         if (FORK)
-            for (int j = lane; j < full; j += 32) {
+            for (int j = lane; j < full; j += wide) {
                 const int pg = prow[j];
                 row[j] = pg;
                 if (is_page(pg, c)) atomicAdd(&c.ref[pg], 1);
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(kBookThreads) take_pages_kernel(const KvView c
             }
             ++first;
         }
-        for (int j = lane; j < more; j += 32) {
+        for (int j = lane; j < more; j += wide) {
             const int pg = taken[first + j];
             row[p0 + j] = pg;
             c.ref[pg] = 1;
