@@ -200,20 +200,20 @@ __device__ __forceinline__ uint32_t ones_below(int n) { return n >= 32 ? ~0u : (
 struct Tile {
     int b, slot, c0, n, len, r0;  // r0: first of the 256 rows (token * G + head)
     int lo, hi;                   // visible cached rows: [lo, hi) and those below `sinks`
-    int sink;                     // leading tiles that only sinks need
+    int sink, start;              // leading tiles that only sinks need; the row where the others start (a box's first)
     int all, first;               // tiles of the whole walk; the first of this CTA's part
-    // of this part's tiles i: those below sinks_to start at row 128 (i + first), the others at 128 (i + skip); rows that
-    // no row of the CTA sees are in tiles up to dead_to and from dead_from on
+    // of this part's tiles i: those below sinks_to start at row 128 (i + first), the others at start + 128 (i + skip);
+    // rows that no row of the CTA sees are in tiles up to dead_to and from dead_from on
     int sinks_to, skip, dead_to, dead_from;
     int tiles_a, tiles_b;         // of this part, per half
     int rows, base, p_hi_a, p_hi_b;  // rows in the tile, position of the sequence's first query, last positions
 };
 __device__ __forceinline__ int tile_row0(const Tile &t, int i) {
-    return (i + (i < t.sinks_to ? t.first : t.skip)) * kKeys;
+    return i < t.sinks_to ? (i + t.first) * kKeys : (i + t.skip) * kKeys + t.start;
 }
 
 // Whether cache tile i may have rows that no row of the CTA sees: the last tile, and where a window has
-// passed the start, the sinks' tiles and the window's first.
+// passed the start, the sinks' tiles and those up to the window.
 __device__ __forceinline__ bool has_dead_rows(const Tile &t, int i) {
     return i >= t.dead_from || i <= t.dead_to;
 }
@@ -265,9 +265,11 @@ __device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, bool chec
     t.p_hi_b = t.base + (t.r0 + t.rows - 1) / a.G;
     t.lo = a.window ? static_cast<int>(max(0LL, static_cast<long long>(p_lo) - a.window + 1)) : 0;
     t.hi = t.p_hi_b + 1;
-    t.sink = t.lo > 0 ? min((min(a.sinks, t.lo) + kKeys - 1) / kKeys, t.lo / kKeys) : 0;
-    t.tiles_a = t.p_hi_a < 0 ? 0 : t.sink + t.p_hi_a / kKeys + 1 - t.lo / kKeys;
-    t.tiles_b = t.rows <= 128 || t.p_hi_b < 0 ? 0 : t.sink + t.p_hi_b / kKeys + 1 - t.lo / kKeys;
+    t.start = t.lo & ~(min(a.c.page_size, kKeys) - 1);
+    t.sink = (min(a.sinks, t.lo) + kKeys - 1) / kKeys;
+    if (t.sink * kKeys >= t.start) t.sink = t.start = 0;  // one walk from the first row
+    t.tiles_a = t.p_hi_a < 0 ? 0 : t.sink + (t.p_hi_a - t.start) / kKeys + 1;
+    t.tiles_b = t.rows <= 128 || t.p_hi_b < 0 ? 0 : t.sink + (t.p_hi_b - t.start) / kKeys + 1;
     t.all = max(t.tiles_a, t.tiles_b);
     t.first = 0;
     return true;
@@ -305,8 +307,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
     t.first = static_cast<int>(static_cast<long long>(t.all) * split / splits);
     const int ntiles = static_cast<int>(static_cast<long long>(t.all) * (split + 1) / splits) - t.first;
     t.sinks_to = t.sink - t.first;
-    t.skip = t.first - t.sink + t.lo / kKeys;
-    t.dead_to = t.lo > 0 ? t.sinks_to : -1;
+    t.skip = t.first - t.sink;
+    t.dead_to = t.lo > 0 ? t.sinks_to + (t.lo - t.start + kKeys - 1) / kKeys - 1 : -1;
     t.dead_from = t.all - 1 - t.first;
     t.tiles_a = min(max(t.tiles_a - t.first, 0), ntiles);
     t.tiles_b = min(max(t.tiles_b - t.first, 0), ntiles);
