@@ -5,15 +5,15 @@
 // The G K query rows of a kv head (G query heads per kv head) share every K and V row read, so the pass
 // moves 4 D bytes per cached row and head for 4 G K D flops: HBM bounds it.
 //
-// Split: the visible 64-row tiles of all (sequence, kv head) pairs form one list; each CTA of a fixed
+// Split: the visible tiles (64 rows at head_dim 128, 128 at 64) of all (sequence, kv head) pairs form one list; each CTA of a fixed
 // grid (the resident CTAs of the card) takes an equal run of it, whatever the mix of lengths. A pair that
 // falls into one run is finished there; a pair that runs cut leaves (m, l, o) per CTA in scratch, and
 // join_kernel, one block per cut and row, adds the parts in run order (the same bits on every call).
 //
-// A CTA is four warps over one tile: K and V rows arrive by 16-byte cp.async, two or three tiles
+// A CTA is four warps over one tile: K and V rows arrive by 16-byte cp.async, one or two tiles
 // ahead, in shared memory whose 16-byte chunks are permuted by chunk ^ (row % 8); mma.sync (m16n8k16, BF16 in,
-// FP32 sums) takes K by ldmatrix and V by ldmatrix.trans. With at most 16 query rows each warp takes 16 of the
-// tile's 64 keys and its own m, l and o, joined at the pair's end; with up to 32 two warps share a key half. mma.sync is enough: at 16 rows the products need about a sixth of its
+// FP32 sums) takes K by ldmatrix and V by ldmatrix.trans. With at most 16 query rows each warp takes a quarter of the
+// tile's keys and its own m, l and o, joined at the pair's end; with up to 32 two warps share a key half. mma.sync is enough: at 16 rows the products need about a sixth of its
 // rate while HBM is saturated. p is rounded to BF16 for the second product (at most 2^-9 of each weight); the sum that o is
 // divided by is that of the rounded p (one more product, with ones), so that the roundings cancel where few keys
 // carry a row, and the one that lse takes is that of the unrounded p.
@@ -24,7 +24,9 @@
 namespace kda {
 namespace {
 
-constexpr int kTile = 64;      // cached rows per tile
+// Cached rows per tile: 32 KB of K and V at either head_dim (at 64, 64 ragged sequences: 104.6 us with 64 rows a tile and
+// four stages, 91.2 with 128 and two)
+__host__ __device__ constexpr int tile_of(int D) { return D == 64 ? 128 : 64; }
 constexpr int kThreads = 128;  // four warps
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -49,6 +51,7 @@ struct Span {
     int len, lo, sink, tiles;  // tiles = 0: the sequence is skipped
     int row0, n;               // its query rows
 };
+template <int kTile>
 __device__ __forceinline__ Span span_of(const DecodeArgs &a, int n, bool &bad) {
     Span s{0, 0, 0, 0, n * a.K, a.K};
     const int slot = a.slots ? a.slots[n] : n;
@@ -70,6 +73,7 @@ __device__ __forceinline__ Span span_of(const DecodeArgs &a, int n, bool &bad) {
     s.tiles = max(1, s.sink + (len + kTile - 1) / kTile - s.lo / kTile);  // an empty one still writes its zeros
     return s;
 }
+template <int kTile>
 __device__ __forceinline__ int tile_row0(const Span &s, int i) {
     return (i < s.sink ? i : i - s.sink + s.lo / kTile) * kTile;
 }
@@ -118,14 +122,15 @@ __device__ __forceinline__ int run_of(long long tiles, int ctas, long long x) {
 
 template <int D, int MT>
 struct DecodeCfg {
+    static constexpr int kTile = tile_of(D);
     static constexpr int KG = 4 / MT;             // key groups: warps that split a tile's keys
     static constexpr int KPW = kTile / KG;        // keys of a tile per warp
-    static constexpr int STAGES = D == 64 ? 4 : 3;
+    static constexpr int STAGES = D == 64 ? 2 : 3;
     static constexpr int HALF = kTile * D * 2;    // bytes of a tile's K (or V)
     static constexpr int ROWS = 16 * MT;
     static constexpr int OFF_ML = STAGES * 2 * HALF;           // [KG][ROWS] of (m, l, l of the rounded p, -)
     static constexpr int OFF_MISC = OFF_ML + KG * ROWS * 16;   // scan, cursor, flags
-    static_assert(KG * ROWS * D * 4 == 2 * HALF, "the warps' o fill the stage of the tile just used");
+    static_assert(KG * ROWS * D * 4 <= 2 * HALF, "the warps' o fill the stage of the tile just used");
     static constexpr int BYTES = OFF_MISC + 256;
     static constexpr int CTAS = D == 64 ? 3 : 2;  // resident per SM
 };
@@ -133,6 +138,7 @@ struct DecodeCfg {
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
     using C = DecodeCfg<D, MT>;
+    constexpr int kTile = tile_of(D);
     extern __shared__ __align__(128) uint8_t sm[];
     float4 *const sml = reinterpret_cast<float4 *>(sm + C::OFF_ML);
     long long *const sscan = reinterpret_cast<long long *>(sm + C::OFF_MISC);  // 4 warp sums
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     long long mine = 0;
     for (int n = n_lo; n < n_hi; ++n) {
         bool bad;
-        mine += span_of(a, n, bad).tiles;
+        mine += span_of<kTile>(a, n, bad).tiles;
         if (bad && blockIdx.x == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
     }
     mine *= hk;
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
         long long at = base;
         for (int n = n_lo; n < n_hi; ++n) {
             bool bad;
-            const long long w = static_cast<long long>(span_of(a, n, bad).tiles) * hk;
+            const long long w = static_cast<long long>(span_of<kTile>(a, n, bad).tiles) * hk;
             if (t_begin < at + w) {
                 scur[0] = n;
                 scur[1] = at;
@@ -195,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     auto open = [&](Cursor &c) {  // the sequence's span; skips sequences without tiles
         bool bad;
         for (; c.n < a.N; ++c.n) {
-            c.s = span_of(a, c.n, bad);
+            c.s = span_of<kTile>(a, c.n, bad);
             if (c.s.tiles > 0) break;
         }
         if (c.n < a.N) c.table = a.c.table + static_cast<size_t>(a.slots ? a.slots[c.n] : c.n) * a.c.max_pages;
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     int chunk = -1, of = -1, here = 0, next = 0;
     auto pages = [&]() {  // for the tile at lc
         if (lc.n >= a.N) return;
-        const int k = tile_row0(lc.s, lc.i) >> (a.c.page_shift + 5);
+        const int k = tile_row0<kTile>(lc.s, lc.i) >> (a.c.page_shift + 5);
         if (lc.n == of && k == chunk) return;
         here = lc.n == of && k == chunk + 1 ? next : fetch(k);
         next = fetch(k + 1);
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
     pages();
     auto load = [&](int stage) {
         if (tl < t_end) {
-            const int j0 = tile_row0(lc.s, lc.i);
+            const int j0 = tile_row0<kTile>(lc.s, lc.i);
             const uint32_t sk = smem_addr(sm + stage * 2 * C::HALF), sv = sk + C::HALF;
             constexpr int CH = D / 8, RP = kThreads / CH;  // 16-byte chunks per row, rows per pass
             const int ch = tid % CH;
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
         load(stage == 0 ? C::STAGES - 1 : stage - 1);
         seg_bad |= tile_bad;
 
-        const int j0 = tile_row0(cc.s, cc.i) + C::KPW * kg;
+        const int j0 = tile_row0<kTile>(cc.s, cc.i) + C::KPW * kg;
         const uint32_t sk = smem_addr(sm + stage * 2 * C::HALF), sv = sk + C::HALF;
         float s[C::KPW / 8][4];
 #pragma unroll
