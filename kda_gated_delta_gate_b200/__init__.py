@@ -589,6 +589,8 @@ class KVCache:
         self.struct = KdaKvCache(_p(k), _p(v), _p(page_table), _p(seq_len), _p(ref), _p(self.scratch),
                                  k.stride(0) if layers > 1 else k[0].numel() if layers else 0, layers, num_pages,
                                  page_size, kv_heads, head_dim, max_seqs, max_pages)
+        self._torch, self._device = torch, k.device.index
+        self._width = kv_heads * head_dim
         self._ref = ctypes.byref(self.struct)
         self._need = {}  # scratch bytes of the attention calls by their sizes
 
@@ -605,50 +607,85 @@ class KVCache:
                    torch.zeros(num_pages, dtype=torch.int32, device=device))
 
 
-def _cache(cache: KVCache):
-    """The cache's struct, for a call on its own device."""
-    import torch
-    if cache.k.device.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {cache.k.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return cache._ref
+def _on(cache: KVCache, stream):
+    """The cache's struct and the stream's handle, for a call on the cache's own device."""
+    dev = cache._torch.cuda.current_device()
+    if dev != cache._device:
+        raise ValueError(f"the cache is on {cache.k.device}, the current device is cuda:{dev}")
+    if stream is not None or _raw_stream is None:
+        return cache._ref, _stream(stream)
+    return cache._ref, _raw_stream(dev)
+
+
+def _ints(cache: KVCache, *ts):
+    """Device pointers of int32 arrays (None stays NULL)."""
+    int32 = cache._torch.int32
+    for t in ts:
+        if t is not None and (t.dtype is not int32 or not t.is_contiguous()):
+            raise ValueError(f"index arrays are contiguous int32 tensors, not {t.dtype}")
+    return [_p(t) for t in ts]
+
+
+def _attn_rows(cache: KVCache, rows: int, d: KdaDims, q, out, lse):
+    """Pointers of q, out and lse after a look at their types and sizes."""
+    n, torch = rows * d.heads, cache._torch
+    size = n * d.head_dim
+    for name, t, dt, size in (("q", q, torch.bfloat16, size), ("out", out, torch.bfloat16, size),
+                              ("lse", lse, torch.float32, n)):
+        if t is not None and (t.dtype is not dt or not t.is_contiguous() or t.numel() < size):
+            raise ValueError(f"{name} is a contiguous {dt} tensor of at least {size} values")
+    return _p(q), _p(out), _p(lse)
 
 
 def kda_kv_reserve(cache: KVCache, slots, add, n: int, stream=None):
     """Room for add[i] more tokens in slot slots[i] (device int32 [n]; slots None: slot i)."""
-    return _call("kda_kv_reserve", _cache(cache), _p(slots), _p(add), n, _stream(stream))
+    ref, st = _on(cache, stream)
+    return _call("kda_kv_reserve", ref, *_ints(cache, slots, add), n, st)
 
 
 def kda_kv_fork(cache: KVCache, parent, child, n: int, stream=None):
     """Slot child[i] becomes a copy of slot parent[i]: full pages shared, a partly filled last page copied."""
-    return _call("kda_kv_fork", _cache(cache), _p(parent), _p(child), n, _stream(stream))
+    ref, st = _on(cache, stream)
+    return _call("kda_kv_fork", ref, *_ints(cache, parent, child), n, st)
 
 
 def kda_kv_truncate(cache: KVCache, slots, new_len, n: int, stream=None):
     """Slot slots[i] keeps its first new_len[i] tokens (0 frees it)."""
-    return _call("kda_kv_truncate", _cache(cache), _p(slots), _p(new_len), n, _stream(stream))
+    ref, st = _on(cache, stream)
+    return _call("kda_kv_truncate", ref, *_ints(cache, slots, new_len), n, st)
 
 
 def kda_kv_compact(cache: KVCache, live=None, stream=None):
     """Move the live pages to the front of the pools; live (device int32 [1]) receives their number."""
-    return _call("kda_kv_compact", _cache(cache), _p(live), _stream(stream))
+    ref, st = _on(cache, stream)
+    return _call("kda_kv_compact", ref, *_ints(cache, live), st)
 
 
-def _rows_stride(name, k_new, v_new) -> int:
-    ld = k_new.stride(0)
-    if k_new.stride(-1) != 1 or v_new.stride(-1) != 1 or (v_new.shape[0] > 1 and v_new.stride(0) != ld):
-        raise ValueError(f"{name}: k_new and v_new are rows of contiguous values with one row stride")
-    if k_new.dim() == 3 and (k_new.stride(1) != k_new.shape[2] or v_new.stride(1) != v_new.shape[2]):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return ld
+def _rows_stride(cache: KVCache, k_new, v_new, rows: int) -> int:
+    """The row stride of k_new and v_new: BF16 rows [rows or more, kv_heads * head_dim] or [.., kv_heads, head_dim]
+    of contiguous values, both of one shape and row stride."""
+    w, bf16, size, step = cache._width, cache._torch.bfloat16, k_new.shape, k_new.stride()
+    if k_new.dtype is not bf16 or v_new.dtype is not bf16 or v_new.shape != size or size[0] < rows:
+        raise ValueError(f"k_new and v_new are bfloat16 tensors of one shape, at least {rows} rows of {w} values")
+    inner = step[1:]
+    if not (len(size) == 2 and size[1] == w and inner == (1,) or
+            len(size) == 3 and size[1] * size[2] == w and inner == (size[2], 1)) or v_new.stride()[1:] != inner:
+        raise ValueError(f"rows of k_new and v_new are {w} contiguous values")
+    if size[0] < 2:
+        return w
+    if v_new.stride(0) != step[0]:
+        raise ValueError("k_new and v_new have one row stride")
+    return step[0]
 
 
 def kda_kv_append(cache: KVCache, layer: int, k_new, v_new, cu_seqlens, slots, B: int, total_tokens: int,
                   stream=None):
     """Packed new K and V rows ([total_tokens, kv_heads * head_dim] or [total_tokens, kv_heads, head_dim], any row
     stride) into the pages of their sequences, whose last tokens they are."""
-    return _call("kda_kv_append", _cache(cache), layer, _p(k_new), _p(v_new),
-                 _rows_stride("kda_kv_append", k_new, v_new), _p(cu_seqlens), _p(slots), B, total_tokens,
-                 _stream(stream))
+    ref, st = _on(cache, stream)
+    ld = _rows_stride(cache, k_new, v_new, total_tokens)
+    return _call("kda_kv_append", ref, layer, _p(k_new), _p(v_new), ld, *_ints(cache, cu_seqlens, slots), B,
+                 total_tokens, st)
 
 
 def kda_attn_decode_scratch_bytes(N: int, K: int, d: KdaDims, cache: KVCache) -> int:
@@ -663,7 +700,7 @@ def kda_attn_prefill_scratch_bytes(B: int, max_rows: int, total_tokens: int, d: 
 def _attn_scratch(fn, key, d: KdaDims, cache: KVCache, stream_handle: int):
     """The stream's cached buffer, of at least fn(*key) bytes; while the current stream is being captured a buffer of the
     graph's own, so that graphs captured one after the other may run at once."""
-    import torch
+    torch = cache._torch
     need = cache._need.get((key, d.heads, d.head_dim))
     if need is None:
         need = cache._need[key, d.heads, d.head_dim] = fn(*key, d, cache)
@@ -676,11 +713,12 @@ def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d
                     sinks: int = 0, lse=None, stream=None, scratch=None):
     """Attention of the last K tokens of each of N sequences over the cache (q, out [N*K, heads, head_dim] BF16,
     lse [N*K, heads] F32 or None). `scratch`: kda_attn_decode_scratch_bytes bytes; a cached buffer when None."""
-    st = _stream(stream)
+    ref, st = _on(cache, stream)
     if scratch is None:
         scratch = _attn_scratch(kda_attn_decode_scratch_bytes, (N, K), d, cache, st)
-    return _call("kda_attn_decode", _cache(cache), layer, _p(q), _p(slots), N, K, window, sinks, _p(out),
-                 _p(lse), _p(scratch), scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
+    pq, po, pl = _attn_rows(cache, N * K, d, q, out, lse)
+    return _call("kda_attn_decode", ref, layer, pq, *_ints(cache, slots), N, K, window, sinks, po,
+                 pl, _p(scratch), scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
 
 
 def kda_attn_prefill(cache: KVCache, layer: int, q, cu_seqlens, slots, B: int, max_rows: int, total_tokens: int, out,
@@ -688,9 +726,10 @@ def kda_attn_prefill(cache: KVCache, layer: int, q, cu_seqlens, slots, B: int, m
     """Attention of packed rows, the last tokens of their sequences, over the cache (q, out
     [total_tokens, heads, head_dim] BF16, lse [total_tokens, heads] F32 or None). `scratch` as for
     kda_attn_decode (kda_attn_prefill_scratch_bytes)."""
-    st = _stream(stream)
+    ref, st = _on(cache, stream)
     if scratch is None:
         scratch = _attn_scratch(kda_attn_prefill_scratch_bytes, (B, max_rows, total_tokens), d, cache, st)
-    return _call("kda_attn_prefill", _cache(cache), layer, _p(q), _p(cu_seqlens), _p(slots), B, max_rows,
-                 total_tokens, window, sinks, _p(out), _p(lse), _p(scratch),
-                 scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
+    pq, po, pl = _attn_rows(cache, total_tokens, d, q, out, lse)
+    return _call("kda_attn_prefill", ref, layer, pq, *_ints(cache, cu_seqlens, slots), B, max_rows,
+                 total_tokens, window, sinks, po, pl, _p(scratch), scratch.numel() * scratch.element_size(),
+                 ctypes.byref(d), st)

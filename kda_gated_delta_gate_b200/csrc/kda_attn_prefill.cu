@@ -605,7 +605,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             unpair(add2(sum[0], sum[1]), sum_lo, sum_hi);
             l += sum_lo + sum_hi;
         }
+        // a half that sees nothing waits for the other, so that both know of a bad page
         if (ok && tiles > 0) ok = wait_or_abort(&ofull[x], C::OWN_P ? (tiles - 1) & 1 : 0, abort, a.status);
+        else if (ok && ntiles > 0) ok = wait_or_abort(&ofull[x ^ 1], 0, abort, a.status);
         tc_fence_after();
         if (splits > 1) {  // this part's l, m and unscaled O; l = -1: a page was none
             const size_t pr = (static_cast<size_t>(slot_id) * hk + h) * a.splits * C::ROWS + static_cast<size_t>(split) * C::ROWS + r;

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvView c, 
     // the sequence of every row: thread b marks its own (the first, should bounds overlap)
     for (int b = tid; b < B; b += kAppendThreads) {
         const int c0 = cu[b], c1 = cu[b + 1];
-        if (c0 < 0 || c1 < c0 || c1 > total) {
+        if (c0 < 0 || c1 < c0 || c1 > total || c1 > end) {
             if (blockIdx.x == 0) atomicExch(status, KDA_ERR_INVALID_ARG);
             continue;
         }

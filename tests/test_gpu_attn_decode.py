@@ -171,3 +171,19 @@ def test_extreme_scores():
     o, l, _ = c.expected()
     assert torch.isfinite(out).all()
     assert np.allclose(lse.double().cpu().numpy(), l, rtol=2.0 ** -17, atol=0)
+
+
+def test_calls_on_another_device_are_refused(monkeypatch):
+    c = Case([20], [1], 4, 2, 64, 16)
+    run(c, 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: c.cache.k.device.index + 1)
+    one = i32([1])
+    for call in (lambda: kda.kda_attn_decode(c.cache, 0, c.qd, None, 1, 1, torch.empty_like(c.qd), c.d, stream=0),
+                 lambda: kda.kda_attn_prefill(c.cache, 0, c.qd, i32([0, 1]), None, 1, 1, 1, torch.empty_like(c.qd), c.d, stream=0),
+                 lambda: kda.kda_kv_reserve(c.cache, None, one, 1, stream=0),
+                 lambda: kda.kda_kv_fork(c.cache, one, one, 1, stream=0),
+                 lambda: kda.kda_kv_truncate(c.cache, None, one, 1, stream=0),
+                 lambda: kda.kda_kv_compact(c.cache, stream=0),
+                 lambda: kda.kda_kv_append(c.cache, 0, c.qd[:, :2], c.qd[:, 2:], i32([0, 1]), None, 1, 1, stream=0)):
+        with pytest.raises(ValueError):
+            call()

@@ -131,12 +131,21 @@ def test_append_edges():
     p.append(0, [0, 1], [7, 1], ids=False)
     p.call("fork", [0], [4])
     p.append(0, [0], [30])                        # its first rows lie in pages that slot 4 shares: not written
-    for cu in ([5, 3, 4], [0, -4, 2], [0, 2, 99], [2 ** 31 - 1, -2 ** 31, 3]):  # no bounds: nothing is read or written outside
+    for cu in ([5, 3, 4], [0, 4, 2], [0, -4, 2], [0, 2, 99], [2 ** 31 - 1, -2 ** 31, 3]):  # no bounds: nothing is read or written outside
         before = p.cache.k.clone()
         rows = torch.zeros((4, 128), dtype=torch.bfloat16, device="cuda")
         kda.kda_kv_append(p.cache, 0, rows, rows, _i32(cu), _i32([5, 5]), 2, 4)
         kda.device_status(clear=True)
         assert torch.equal(p.cache.k, before)
+
+
+def test_append_with_decreasing_bounds_writes_nothing_it_has_not_read():
+    p = Pair(pages=10, page=16, seqs=3, max_pages=4)
+    p.call("reserve", [0, 1], [16, 16])
+    before = p.cache.k.clone()
+    rows = torch.ones((6, 128), dtype=torch.bfloat16, device="cuda")
+    kda.kda_kv_append(p.cache, 0, rows, rows, _i32([0, 6, 2]), _i32([0, 1]), 2, 6)
+    assert kda.device_status(clear=True) == 1 and torch.equal(p.cache.k, before)
 
 
 def test_large_pools_and_many_slots():

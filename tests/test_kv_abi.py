@@ -121,6 +121,32 @@ def test_cache_object_checks_its_tensors(L):
                dict(v=torch.zeros(2, 4, 16, 2, 64, dtype=torch.bfloat16).transpose(2, 3))):
         with pytest.raises(ValueError):
             make(**kw)
+
+
+def test_binding_checks_types_and_sizes():
+    bf = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16)
+    d = kda.dims(4, 64)
+    c = kda.KVCache(bf(1, 4, 2, 16, 64), bf(1, 4, 2, 16, 64), torch.zeros(3, 5, dtype=torch.int32),
+                    torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32))
+    stride = lambda k, v: kda._rows_stride(c, k, v, 4)
+    wide = bf(4, 384)
+    assert stride(wide[:, 128:256], wide[:, 256:]) == 384
+    assert stride(bf(5, 2, 64), bf(5, 2, 64)) == 128
+    assert stride(bf(4, 6, 64)[:, 2:4], bf(4, 6, 64)[:, 4:]) == 384
+    assert kda._rows_stride(c, wide[:1, :128], bf(1, 128), 1) == 128
+    for k in (bf(4, 128).float(), bf(3, 128), bf(4, 64), bf(128, 4).T, bf(4, 64, 2).transpose(1, 2), bf(4, 256)[:, ::2],
+              bf(4, 2, 128)[:, :, :64], bf(5, 128)):
+        with pytest.raises(ValueError):
+            stride(k, bf(4, 128))
     with pytest.raises(ValueError):
-        kda._rows_stride("append", torch.zeros(4, 8).T, torch.zeros(4, 8).T)
-    assert kda._rows_stride("append", torch.zeros(4, 24)[:, 8:16], torch.zeros(4, 24)[:, 16:]) == 24
+        stride(bf(4, 128), wide[:, :128])  # two row strides
+    kda._attn_rows(c, 3, d, bf(3, 4, 64), bf(3, 4, 64), None)
+    for q, o, l in ((bf(3, 4, 32), bf(3, 4, 64), None), (bf(3, 4, 64).float(), bf(3, 4, 64), None),
+                    (bf(3, 4, 128)[:, :, ::2], bf(3, 4, 64), None), (bf(3, 4, 64), bf(2, 4, 64), None),
+                    (bf(3, 4, 64), bf(3, 4, 64), torch.zeros(3, 3)), (bf(3, 4, 64), bf(3, 4, 64), bf(3, 4))):
+        with pytest.raises(ValueError):
+            kda._attn_rows(c, 3, d, q, o, l)
+    assert kda._ints(c, None, torch.zeros(2, dtype=torch.int32))[0] is None
+    for t in (torch.zeros(2, dtype=torch.int64), torch.zeros(4, dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError):
+            kda._ints(c, t)
