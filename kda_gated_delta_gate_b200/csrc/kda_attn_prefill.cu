@@ -300,20 +300,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
     const int hk = a.c.kv_heads, split = blockIdx.x % a.splits, h = blockIdx.x / a.splits % hk;
     const int slot_id = a.nslots - 1 - static_cast<int>(blockIdx.x / a.splits / hk);  // the longest walks first
 
-    Tile t;
-    if (!locate<C::ROWS>(a, slot_id, blockIdx.x == 0 && warp == 0, t)) return;
-    const int splits = parts_of(a, t);
-    if (split >= splits) return;
-    t.first = static_cast<int>(static_cast<long long>(t.all) * split / splits);
-    const int ntiles = static_cast<int>(static_cast<long long>(t.all) * (split + 1) / splits) - t.first;
-    t.sinks_to = t.sink - t.first;
-    t.skip = t.first - t.sink;
-    t.dead_to = t.lo > 0 ? t.sinks_to + (t.lo - t.start + kKeys - 1) / kKeys - 1 : -1;
-    t.dead_from = t.all - 1 - t.first;
-    t.tiles_a = min(max(t.tiles_a - t.first, 0), ntiles);
-    t.tiles_b = min(max(t.tiles_b - t.first, 0), ntiles);
-
-    if (tid == 0) {
+    // TMEM and barriers by two of the warps that do not compute, under every warp's search for the tile
+    if (warp == W + 2 && lane == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -336,6 +324,24 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
         tmem_alloc(tmem_slot, C::TMEM);
         tmem_relinquish();
     }
+
+    Tile t;
+    const bool found = locate<C::ROWS>(a, slot_id, blockIdx.x == 0 && warp == 0, t);
+    const int splits = found ? parts_of(a, t) : 0;
+    if (split >= splits) {  // nothing to do here but to give the columns back
+        __syncthreads();
+        if (warp == W + 1) tmem_dealloc(*tmem_slot, C::TMEM);
+        return;
+    }
+    t.first = static_cast<int>(static_cast<long long>(t.all) * split / splits);
+    const int ntiles = static_cast<int>(static_cast<long long>(t.all) * (split + 1) / splits) - t.first;
+    t.sinks_to = t.sink - t.first;
+    t.skip = t.first - t.sink;
+    t.dead_to = t.lo > 0 ? t.sinks_to + (t.lo - t.start + kKeys - 1) / kKeys - 1 : -1;
+    t.dead_from = t.all - 1 - t.first;
+    t.tiles_a = min(max(t.tiles_a - t.first, 0), ntiles);
+    t.tiles_b = min(max(t.tiles_b - t.first, 0), ntiles);
+
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
