@@ -5,19 +5,25 @@
 // The G K query rows of a kv head (G query heads per kv head) share every K and V row read, so the pass
 // moves 4 D bytes per cached row and head for 4 G K D flops: HBM bounds it.
 //
-// Split: the visible tiles (64 rows at head_dim 128, 128 at 64) of all (sequence, kv head) pairs form one list; each CTA of a fixed
-// grid (the resident CTAs of the card) takes an equal run of it, whatever the mix of lengths. A pair that
+// Split: the visible tiles (64 rows at head_dim 128, 128 at 64) of all (sequence, kv head) pairs form one list; each CTA
+// of a fixed grid (the resident CTAs of the card) takes an equal run of it, whatever the mix of lengths. A pair that
 // falls into one run is finished there; a pair that runs cut leaves (m, l, o) per CTA in scratch, and
-// join_kernel, one block per cut and row, adds the parts in run order (the same bits on every call).
+// join_kernel adds the parts in a fixed order (the same bits on every call).
 //
-// A CTA is four warps over one tile: K and V rows arrive by 16-byte cp.async, one or two tiles
-// ahead, in shared memory whose 16-byte chunks are permuted by chunk ^ (row % 8); mma.sync (m16n8k16, BF16 in,
-// FP32 sums) takes K by ldmatrix and V by ldmatrix.trans. With at most 16 query rows each warp takes a quarter of the
-// tile's keys and its own m, l and o, joined at the pair's end; with up to 32 two warps share a key half. mma.sync is enough: at 16 rows the products need about a sixth of its
-// rate while HBM is saturated. p is rounded to BF16 for the second product (at most 2^-9 of each weight); the sum that o is
-// divided by is that of the rounded p (one more product, with ones), so that the roundings cancel where few keys
-// carry a row, and the one that lse takes is that of the unrounded p.
+// A CTA is four warps over one tile: K and V rows arrive by 16-byte cp.async, one or two tiles ahead, in shared memory whose
+// 16-byte chunks are permuted by chunk ^ (row % 8); mma.sync (m16n8k16, BF16 in, FP32 sums) takes them by ldmatrix.
+// With at most 16 query rows each warp takes a quarter of the tile's keys and its own m, l and o, joined at the pair's
+// end; with up to 32 two warps share a key half. With at most 8 the products are turned round (RowsShort). mma.sync is
+// enough: at 16 rows the products need about a sixth of its rate while HBM is saturated.
+// p is rounded to BF16 for the second product (at most 2^-9 of each weight); the sum that o is divided by is that of the
+// rounded p (one more product, with ones), so that the roundings cancel where few keys carry a row, and the one that
+// lse takes is that of the unrounded p.
+//
+// Measured (device time, HBM 6545 GB/s): 8 x 65500 tokens, 8 kv heads of 128, 4 rows per kv head: 316 us = 6.8 TB/s; 64
+// sequences of 125 to 8000 tokens, 16 rows: 188 us = 5.7 TB/s; one sequence of 4096: 11.9 us, nearly all of it the latency
+// of two launches and of the reads that depend on one another (slot, length, table, K, parts).
 #include <algorithm>
+#include <type_traits>
 
 #include "kv.cuh"
 
@@ -105,6 +111,19 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// An 8 x 8 matrix of 16-bit values, a row's two neighbours per thread, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+constexpr uint32_t kOnes = 0x3f803f80u;  // two BF16 ones
+// The score in base 2 of cached row j for a row at position p; -inf where it is hidden.
+__device__ __forceinline__ float seen_score(const DecodeArgs &a, float s, bool all_seen, int j, int p) {
+    s *= a.scale2;
+    if (all_seen) return s;
+    return j <= p && (!a.window || j > p - a.window || j < a.sinks) ? s : -INFINITY;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
@@ -120,24 +139,269 @@ __device__ __forceinline__ int run_of(long long tiles, int ctas, long long x) {
     return static_cast<int>(((x + 1) * ctas + tiles - 1) / tiles) - 1;
 }
 
+// A warp's share of a tile in the two forms. Both hold, for the warp's keys, the rows' queries, m, l, the sums lp of the
+// rounded p and o, and have:
+//   fetch   the rows' queries and positions (called before the last pair's results are written, so that the loads run
+//           under that);  begin  an empty softmax;  tile  one tile;  put  m, l, lp to ml and o to the join buffer,
+//           where channel d of row r lies at place(r, d): groups of eight channels are permuted so that what a warp writes
+//           at once goes to different banks.
+
+// Up to 8 rows: K q^T (keys x rows) and V^T p^T (channels x rows), rows on the products' short side, so that none is
+// spent on padding to 16. Thread: rows 2 (lane % 4) + e. Against the other form (8 x 65500 tokens, 4 rows per kv head):
+// 315 us against 320, and 316 against 340 once the card has warmed up, since it does half the products.
+template <int D>
+struct RowsShort {
+    static constexpr int KG = 4, ROWS = 8, KPW = tile_of(D) / KG;
+    uint32_t qf[D / 16][2];
+    float o[D / 16][4], m[2], l[2], lp[4];
+    int pos[2];
+    static __device__ __forceinline__ int keys0(int warp) { return KPW * warp; }
+    static __device__ __forceinline__ int place(int r, int d) { return r * D + (d ^ (((r >> 1) & 3) << 3)); }
+    __device__ __forceinline__ void fetch(const DecodeArgs &a, const Span &sp, int h, int, int lane) {
+        const int rows = a.G * sp.n, r = lane >> 2, t = r / a.G;
+        const uint16_t *const q = a.q + (static_cast<size_t>(sp.row0 + t) * a.heads + static_cast<size_t>(h) * a.G + (r - t * a.G)) * D +
+                                  2 * (lane & 3);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            qf[ks][0] = r < rows ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * ks)) : 0u;
+            qf[ks][1] = r < rows ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * ks + 8)) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) pos[e] = sp.len - sp.n + min((2 * (lane & 3) + e) / a.G, sp.n - 1);
+    }
+    __device__ __forceinline__ void begin() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+        lp[0] = lp[1] = lp[2] = lp[3] = 0.f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+    }
+    // j0: the warp's first key; all_seen: every row sees all of its keys
+    __device__ __forceinline__ void tile(const DecodeArgs &a, uint32_t sk, uint32_t sv, int j0, bool all_seen, int warp, int lane) {
+        float s[KPW / 16][4], top[2] = {-INFINITY, -INFINITY}, safe[2];
+#pragma unroll
+        for (int kb = 0; kb < KPW / 16; ++kb) {
+            s[kb][0] = s[kb][1] = s[kb][2] = s[kb][3] = 0.f;
+            // matrices: keys +0..7 / +8..15 (lane bit 3), channels +0..7 / +8..15 (lane bit 4)
+            const int r = keys0(warp) + 16 * kb + (lane & 15);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t k[4];
+                ldsm4(sk + r * D * 2 + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4), k);
+                mma16816(s[kb], k, qf[ks][0], qf[ks][1]);
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < KPW / 16; ++kb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[kb][e] = seen_score(a, s[kb][e], all_seen, j0 + 16 * kb + (lane >> 2) + 8 * (e >> 1), pos[e & 1]);
+                top[e & 1] = fmaxf(top[e & 1], s[kb][e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], w));
+            const float mn = fmaxf(m[e], top[e]);
+            safe[e] = mn == -INFINITY ? 0.f : mn;
+            const float f = ex2(m[e] - safe[e]);
+            m[e] = mn;
+            l[e] *= f;
+            lp[e] *= f;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                o[d][e] *= f;
+                o[d][2 + e] *= f;
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < KPW / 16; ++kb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[kb][e] = ex2(s[kb][e] - safe[e & 1]);
+                l[e & 1] += s[kb][e];
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < KPW / 16; ++kb) {
+            // p of 16 keys: from (key, two rows) to (row, two keys) per thread
+            const uint32_t p0 = transpose8(pack_bf16(s[kb][0], s[kb][1])), p1 = transpose8(pack_bf16(s[kb][2], s[kb][3]));
+            const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
+            mma16816(lp, ones, p0, p1);
+            // matrices: keys +0..7 / +8..15 (lane bit 4), channels +0..7 / +8..15 (lane bit 3)
+            const int r = keys0(warp) + 16 * kb + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                uint32_t v[4];
+                ldsm4t(sv + r * D * 2 + (((2 * d + ((lane >> 3) & 1)) ^ (r & 7)) << 4), v);
+                mma16816(o[d], v, p0, p1);
+            }
+        }
+    }
+    __device__ __forceinline__ void put_sums(float4 *ml, int warp, int lane) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], w);
+            if (lane < 4) ml[warp * ROWS + 2 * lane + e] = make_float4(m[e], l[e], lp[e], 0.f);
+        }
+    }
+    __device__ __forceinline__ void put_o(float *so, int rows, int warp, int lane) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = 2 * (lane & 3) + (e & 1);
+            if (r < rows) {
+                float *const w = so + (warp * ROWS + r) * D + (lane >> 2);
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) w[8 * ((2 * d + (e >> 1)) ^ (lane & 3))] = o[d][e];
+            }
+        }
+    }
+};
+
+// Up to 16 MT rows: q K^T (rows x keys) and p V (rows x channels). Thread: rows 16 (warp % MT) + lane / 4 and + 8; MT warps
+// share a key group.
 template <int D, int MT>
+struct RowsLong {
+    static constexpr int KG = 4 / MT, ROWS = 16 * MT, KPW = tile_of(D) / KG;
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4], m[2], l[2], lp[4];
+    int pos[2];
+    static __device__ __forceinline__ int keys0(int warp) { return KPW * (warp / MT); }
+    static __device__ __forceinline__ int place(int r, int d) { return r * D + (d ^ ((r & 3) << 3)); }
+    static __device__ __forceinline__ int row(int warp, int lane, int e) { return 16 * (warp % MT) + (lane >> 2) + 8 * e; }
+    __device__ __forceinline__ void fetch(const DecodeArgs &a, const Span &sp, int h, int warp, int lane) {
+        const int rows = a.G * sp.n;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = row(warp, lane, e), t = r / a.G;
+            const uint16_t *const q = a.q + (static_cast<size_t>(sp.row0 + t) * a.heads + static_cast<size_t>(h) * a.G + (r - t * a.G)) * D +
+                                      2 * (lane & 3);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                qf[ks][e] = r < rows ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * ks)) : 0u;
+                qf[ks][2 + e] = r < rows ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * ks + 8)) : 0u;
+            }
+            pos[e] = sp.len - sp.n + min(t, sp.n - 1);
+        }
+    }
+    __device__ __forceinline__ void begin() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+        lp[0] = lp[1] = lp[2] = lp[3] = 0.f;
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+    }
+    __device__ __forceinline__ void tile(const DecodeArgs &a, uint32_t sk, uint32_t sv, int j0, bool all_seen, int warp, int lane) {
+        float s[KPW / 8][4], top[2] = {-INFINITY, -INFINITY}, safe[2];
+#pragma unroll
+        for (int nb = 0; nb < KPW / 16; ++nb) {
+            float(&s0)[4] = s[2 * nb], (&s1)[4] = s[2 * nb + 1];
+            s0[0] = s0[1] = s0[2] = s0[3] = s1[0] = s1[1] = s1[2] = s1[3] = 0.f;
+            // matrices: keys +0..7 / +8..15 (lane bit 4), channels +0..7 / +8..15 (lane bit 3)
+            const int r = keys0(warp) + 16 * nb + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const int ch = 2 * ks + ((lane >> 3) & 1);
+                uint32_t b[4];
+                ldsm4(sk + r * D * 2 + ((ch ^ (r & 7)) << 4), b);
+                mma16816(s0, qf[ks], b[0], b[1]);
+                mma16816(s1, qf[ks], b[2], b[3]);
+            }
+        }
+#pragma unroll
+        for (int nb = 0; nb < KPW / 8; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[nb][e] = seen_score(a, s[nb][e], all_seen, j0 + 8 * nb + 2 * (lane & 3) + (e & 1), pos[e >> 1]);
+                top[e >> 1] = fmaxf(top[e >> 1], s[nb][e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+            const float mn = fmaxf(m[e], top[e]);
+            safe[e] = mn == -INFINITY ? 0.f : mn;
+            const float f = ex2(m[e] - safe[e]);
+            m[e] = mn;
+            l[e] *= f;
+            lp[2 * e] *= f;
+            lp[2 * e + 1] *= f;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+                o[d][2 * e] *= f;
+                o[d][2 * e + 1] *= f;
+            }
+        }
+#pragma unroll
+        for (int nb = 0; nb < KPW / 8; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[nb][e] = ex2(s[nb][e] - safe[e >> 1]);
+                l[e >> 1] += s[nb][e];
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < KPW / 16; ++kb) {
+            const uint32_t p[4] = {pack_bf16(s[2 * kb][0], s[2 * kb][1]), pack_bf16(s[2 * kb][2], s[2 * kb][3]),
+                                   pack_bf16(s[2 * kb + 1][0], s[2 * kb + 1][1]),
+                                   pack_bf16(s[2 * kb + 1][2], s[2 * kb + 1][3])};
+            mma16816(lp, p, kOnes, kOnes);
+            const int r = keys0(warp) + 16 * kb + (lane & 15);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                const int ch = 2 * d + (lane >> 4);
+                uint32_t b[4];
+                ldsm4t(sv + r * D * 2 + ((ch ^ (r & 7)) << 4), b);
+                mma16816(o[2 * d], p, b[0], b[1]);
+                mma16816(o[2 * d + 1], p, b[2], b[3]);
+            }
+        }
+    }
+    __device__ __forceinline__ void put_sums(float4 *ml, int warp, int lane) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            if ((lane & 3) == 0) ml[warp / MT * ROWS + row(warp, lane, e)] = make_float4(m[e], l[e], lp[2 * e], 0.f);
+        }
+    }
+    __device__ __forceinline__ void put_o(float *so, int rows, int warp, int lane) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = row(warp, lane, e);
+            if (r < rows) {
+                float *const w = so + (warp / MT * ROWS + r) * D + 2 * (lane & 3);
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d)
+                    *reinterpret_cast<float2 *>(w + 8 * (d ^ (r & 3))) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
+            }
+        }
+    }
+};
+
+template <int D, int R>
+using Rows = std::conditional_t<R == 8, RowsShort<D>, RowsLong<D, R == 32 ? 2 : 1>>;
+
+// D: head_dim; R: the most query rows per kv head (8, 16 or 32).
+template <int D, int R>
 struct DecodeCfg {
     static constexpr int kTile = tile_of(D);
-    static constexpr int KG = 4 / MT;             // key groups: warps that split a tile's keys
-    static constexpr int KPW = kTile / KG;        // keys of a tile per warp
+    static constexpr int KG = Rows<D, R>::KG;     // key groups: warps that split a tile's keys
     static constexpr int STAGES = D == 64 ? 2 : 3;
     static constexpr int HALF = kTile * D * 2;    // bytes of a tile's K (or V)
-    static constexpr int ROWS = 16 * MT;
-    static constexpr int OFF_ML = STAGES * 2 * HALF;           // [KG][ROWS] of (m, l, l of the rounded p, -)
-    static constexpr int OFF_MISC = OFF_ML + KG * ROWS * 16;   // scan, cursor, flags
-    static_assert(KG * ROWS * D * 4 <= 2 * HALF, "the warps' o fill the stage of the tile just used");
+    static constexpr int OFF_ML = STAGES * 2 * HALF;        // [KG][R] of (m, l, l of the rounded p, -)
+    static constexpr int OFF_MISC = OFF_ML + KG * R * 16;   // scan, cursor, flags
+    static_assert(KG * R * D * 4 <= 2 * HALF, "the warps' o go into the stage of the tile just used");
     static constexpr int BYTES = OFF_MISC + 256;
     static constexpr int CTAS = D == 64 ? 3 : 2;  // resident per SM
 };
 
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
-    using C = DecodeCfg<D, MT>;
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, DecodeCfg<D, R>::CTAS) decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using C = DecodeCfg<D, R>;
     constexpr int kTile = tile_of(D);
     extern __shared__ __align__(128) uint8_t sm[];
     float4 *const sml = reinterpret_cast<float4 *>(sm + C::OFF_ML);
@@ -285,45 +549,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    // ---- per warp: rows 16 mt .., keys KPW kg ..
-    const int mt = warp % MT, kg = warp / MT;
-    const int ra = 16 * mt + (lane >> 2), rb = ra + 8;  // this thread's two rows
-    uint32_t qf[D / 16][4];
-    float o[D / 8][4], m[2], l[2], lp[4];  // lp: sums of the rounded p (0, 2: this thread's rows)
-    int pos[2];
+    Rows<D, R> w;
     bool seg_bad = false;
-    // the rows' queries and positions; called before the last pair's results are written, so that the loads run under that
-    auto fetch_rows = [&]() {
-        const int rows = a.G * cc.s.n;
-        const uint16_t *const qn = a.q + (static_cast<size_t>(cc.s.row0) * a.heads + static_cast<size_t>(cc.h) * a.G) * D;
-        const int ta = ra / a.G, tb = rb / a.G;
-        const uint16_t *const qa = qn + (static_cast<size_t>(ta) * a.heads + (ra - ta * a.G)) * D + 2 * (lane & 3);
-        const uint16_t *const qb = qn + (static_cast<size_t>(tb) * a.heads + (rb - tb * a.G)) * D + 2 * (lane & 3);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            qf[ks][0] = ra < rows ? __ldg(reinterpret_cast<const uint32_t *>(qa + 16 * ks)) : 0u;
-            qf[ks][1] = rb < rows ? __ldg(reinterpret_cast<const uint32_t *>(qb + 16 * ks)) : 0u;
-            qf[ks][2] = ra < rows ? __ldg(reinterpret_cast<const uint32_t *>(qa + 16 * ks + 8)) : 0u;
-            qf[ks][3] = rb < rows ? __ldg(reinterpret_cast<const uint32_t *>(qb + 16 * ks + 8)) : 0u;
-        }
-        pos[0] = cc.s.len - cc.s.n + min(ta, cc.s.n - 1);
-        pos[1] = cc.s.len - cc.s.n + min(tb, cc.s.n - 1);
-    };
-    auto begin_pair = [&]() {
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
-        lp[0] = lp[1] = lp[2] = lp[3] = 0.f;
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
-        seg_bad = false;
-    };
-
 #pragma unroll 1
     for (int s = 0; s < C::STAGES - 1; ++s) load(s);
     int stage = 0;
     long long seg0 = t_begin;  // where the current pair's tiles in this run begin
-    fetch_rows();
-    begin_pair();
+    w.fetch(a, cc.s, cc.h, warp, lane);
+    w.begin();
 #pragma unroll 1
     for (long long t = t_begin; t < t_end; ++t) {
         asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 2) : "memory");
@@ -332,83 +565,12 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
         load(stage == 0 ? C::STAGES - 1 : stage - 1);
         seg_bad |= tile_bad;
 
-        const int j0 = tile_row0<kTile>(cc.s, cc.i) + C::KPW * kg;
-        const uint32_t sk = smem_addr(sm + stage * 2 * C::HALF), sv = sk + C::HALF;
-        float s[C::KPW / 8][4];
-#pragma unroll
-        for (int nb = 0; nb < C::KPW / 16; ++nb) {
-            float(&s0)[4] = s[2 * nb], (&s1)[4] = s[2 * nb + 1];
-            s0[0] = s0[1] = s0[2] = s0[3] = s1[0] = s1[1] = s1[2] = s1[3] = 0.f;
-            // matrices: keys +0..7 / +8..15 (lane bit 4), channels +0..7 / +8..15 (lane bit 3)
-            const int r = C::KPW * kg + 16 * nb + (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const int ch = 2 * ks + ((lane >> 3) & 1);
-                uint32_t b[4];
-                ldsm4(sk + r * D * 2 + ((ch ^ (r & 7)) << 4), b);
-                mma16816(s0, qf[ks], b[0], b[1]);
-                mma16816(s1, qf[ks], b[2], b[3]);
-            }
-        }
-        // the whole tile is visible to every row, or each weight is looked at
-        const bool all_seen = j0 + C::KPW <= cc.s.len - cc.s.n + 1 && (!a.window || j0 > cc.s.len - 1 - a.window);
-        float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int nb = 0; nb < C::KPW / 8; ++nb) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float y = s[nb][e] * a.scale2;
-                if (!all_seen) {
-                    const int j = j0 + 8 * nb + 2 * (lane & 3) + (e & 1), p = pos[e >> 1];
-                    const bool seen = j <= p && (!a.window || j > p - a.window || j < a.sinks);
-                    y = seen ? y : -INFINITY;
-                }
-                s[nb][e] = y;
-                top[e >> 1] = fmaxf(top[e >> 1], y);
-            }
-        }
-        float safe[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-            const float mn = fmaxf(m[e], top[e]);
-            safe[e] = mn == -INFINITY ? 0.f : mn;
-            const float f = ex2(m[e] - safe[e]);
-            m[e] = mn;
-            l[e] *= f;
-            lp[2 * e] *= f;
-            lp[2 * e + 1] *= f;
-#pragma unroll
-            for (int d = 0; d < D / 8; ++d) {
-                o[d][2 * e] *= f;
-                o[d][2 * e + 1] *= f;
-            }
-        }
-#pragma unroll
-        for (int nb = 0; nb < C::KPW / 8; ++nb) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[nb][e] = ex2(s[nb][e] - safe[e >> 1]);
-                l[e >> 1] += s[nb][e];
-            }
-        }
-#pragma unroll
-        for (int kb = 0; kb < C::KPW / 16; ++kb) {
-            const uint32_t p[4] = {pack_bf16(s[2 * kb][0], s[2 * kb][1]), pack_bf16(s[2 * kb][2], s[2 * kb][3]),
-                                   pack_bf16(s[2 * kb + 1][0], s[2 * kb + 1][1]),
-                                   pack_bf16(s[2 * kb + 1][2], s[2 * kb + 1][3])};
-            mma16816(lp, p, 0x3f803f80u, 0x3f803f80u);  // p times ones
-            const int r = C::KPW * kg + 16 * kb + (lane & 15);
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-                const int ch = 2 * d + (lane >> 4);
-                uint32_t b[4];
-                ldsm4t(sv + r * D * 2 + ((ch ^ (r & 7)) << 4), b);
-                mma16816(o[2 * d], p, b[0], b[1]);
-                mma16816(o[2 * d + 1], p, b[2], b[3]);
-            }
-        }
+        const uint32_t sk = smem_addr(sm + stage * 2 * C::HALF);
+        constexpr int KPW = Rows<D, R>::KPW;
+        const int j0 = tile_row0<kTile>(cc.s, cc.i) + Rows<D, R>::keys0(warp);
+        // the warp's keys are all visible to every row, or each weight is looked at
+        const bool all_seen = j0 + KPW <= cc.s.len - cc.s.n + 1 && (!a.window || j0 > cc.s.len - 1 - a.window);
+        w.tile(a, sk, sk + C::HALF, j0, all_seen, warp, lane);
         float *const so = reinterpret_cast<float *>(sm + stage * 2 * C::HALF);  // free once all warps are here
         if (++stage == C::STAGES) stage = 0;
 
@@ -419,28 +581,12 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
             const int slot = seg0 == t_begin ? 0 : 1, rows = a.G * cc.s.n, h = cc.h, row0 = cc.s.row0;
             if (t + 1 < t_end) {
                 step(cc);
-                fetch_rows();
+                w.fetch(a, cc.s, cc.h, warp, lane);
                 seg0 = t + 1;
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-                if ((lane & 3) == 0) sml[kg * C::ROWS + (e ? rb : ra)] = make_float4(m[e], l[e], lp[2 * e], 0.f);
-            }
+            w.put_sums(sml, warp, lane);
             __syncthreads();
-            // every warp's o, [KG][ROWS][D], groups of eight channels permuted by row so that the rows that a warp writes at
-            // once spread over the banks
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = e ? rb : ra;
-                if (r < rows) {
-                    float *const w = so + (kg * C::ROWS + r) * D + 2 * (lane & 3);
-#pragma unroll
-                    for (int d = 0; d < D / 8; ++d)
-                        *reinterpret_cast<float2 *>(w + 8 * (d ^ (r & 3))) = make_float2(o[d][2 * e], o[d][2 * e + 1]);
-                }
-            }
+            w.put_o(so, rows, warp, lane);
             __syncthreads();
             for (int i = tid; i < rows * (D / 4); i += kThreads) {
                 const int r = i / (D / 4), d = 4 * (i % (D / 4));
@@ -448,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
                 float4 ml[C::KG], v = make_float4(0.f, 0.f, 0.f, 0.f), u[C::KG];
 #pragma unroll
                 for (int g = 0; g < C::KG; ++g) {
-                    ml[g] = sml[g * C::ROWS + r];
-                    u[g] = *reinterpret_cast<const float4 *>(so + (g * C::ROWS + r) * D + (d ^ ((r & 3) << 3)));
+                    ml[g] = sml[g * R + r];
+                    u[g] = *reinterpret_cast<const float4 *>(so + g * R * D + Rows<D, R>::place(r, d));
                     top_all = fmaxf(top_all, ml[g].x);
                 }
                 const float ref = top_all == -INFINITY ? 0.f : top_all;
@@ -481,7 +627,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, MT>::CTAS) decode_kerne
             }
             if (seg_bad && tid == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
             // the next tile's barrier comes before anything goes into so or sml again
-            begin_pair();
+            w.begin();
+            seg_bad = false;
         } else {
             ++cc.i;
         }
@@ -569,12 +716,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     }
 }
 
-template <int D, int MT>
+template <int D, int R>
 int launch_decode(const DecodeArgs &a, int grid, cudaStream_t s) {
-    using C = DecodeCfg<D, MT>;
+    using C = DecodeCfg<D, R>;
     static std::atomic<unsigned long long> attr{0};
-    KDA_TRY(smem_opt_in(decode_kernel<D, MT>, C::BYTES, attr, true));
-    decode_kernel<D, MT><<<grid, kThreads, C::BYTES, s>>>(a);
+    KDA_TRY(smem_opt_in(decode_kernel<D, R>, C::BYTES, attr, true));
+    decode_kernel<D, R><<<grid, kThreads, C::BYTES, s>>>(a);
     KDA_TRY(launch_status());
     if (grid < 2) return KDA_OK;
     const int rows = a.G * a.K;
@@ -585,7 +732,6 @@ int launch_decode(const DecodeArgs &a, int grid, cudaStream_t s) {
 }
 
 int ctas_per_sm(int D) { return D == 64 ? 3 : 2; }
-int m_tiles(int rows) { return rows <= 16 ? 1 : 2; }
 
 size_t info_bytes(int grid) { return (1 + 5 * static_cast<size_t>(grid)) * 8 / 16 * 16 + 16; }
 
@@ -618,14 +764,17 @@ int attn_rows(const kda_kv_cache *cache, int layer, const uint16_t *q, const int
     a.window = window < a.c.max_pages * a.c.page_size ? window : 0;
     a.sinks = std::min(sinks, a.c.max_pages * a.c.page_size);
     a.scale2 = dims->scale * kLog2e;
-    const int rows = a.G * K, mt = m_tiles(rows), D = dims->head_dim;
+    const int rows = a.G * K, D = dims->head_dim;
     const int grid = ctas_per_sm(D) * num_sms();
     char *const p = static_cast<char *>(scratch);
     a.info = reinterpret_cast<long long *>(p);
     a.part_o = reinterpret_cast<float *>(p + info_bytes(grid));
     a.part_ml = a.part_o + static_cast<size_t>(grid) * 2 * rows * D;
-    if (D == 128) return mt == 1 ? launch_decode<128, 1>(a, grid, s) : launch_decode<128, 2>(a, grid, s);
-    return mt == 1 ? launch_decode<64, 1>(a, grid, s) : launch_decode<64, 2>(a, grid, s);
+    if (D == 128)
+        return rows <= 8 ? launch_decode<128, 8>(a, grid, s)
+                         : (rows <= 16 ? launch_decode<128, 16>(a, grid, s) : launch_decode<128, 32>(a, grid, s));
+    return rows <= 8 ? launch_decode<64, 8>(a, grid, s)
+                     : (rows <= 16 ? launch_decode<64, 16>(a, grid, s) : launch_decode<64, 32>(a, grid, s));
 }
 
 namespace {
