@@ -1,30 +1,38 @@
 // Attention of packed query rows over their paged cache (include/kda.h, kda_attn_prefill).
 //
-// Per (sequence, kv head) the n query tokens of G query heads are n G rows (token major, then head), cut into
-// tiles of 256; a CTA takes one such tile and walks the visible 128-row tiles of the cache once, with the
-// softmax's running reference m and sum l: S = Q K^T, P = 2^(scale log2(e) S - m), l += rowsum P, O += P V.
-// 4 D flops and one exponential per (row, cached row) pair: the tensor cores bound it at D = 128 (2 x 512
-// cycles of MMA per 128 x 128 x 128 pair of products against 1024 cycles of exponentials), the exponentials at D = 64.
+// Per (sequence, kv head) the n query tokens of G query heads are n G rows (token major, then head), cut into tiles of
+// 256 (128 at head_dim 64); a CTA takes one such tile and walks the visible rows of the cache once, 128 at a time, with
+// the softmax's running reference m and sum l: S = Q K^T, P = 2^(scale log2(e) S - m), l += rowsum P, O += P V.
+// 4 D flops and one exponential per (row, cached row) pair: the tensor cores bound it at D = 128 (512 cycles of MMA for each
+// 128 x 128 x 128 product; 256 rows by 128 keys are four of them and 2048 cycles of exponentials), the exponentials at D = 64.
 //
-// Twelve warps, one CTA per SM (the softmax warps take registers that the other warpgroup gives up: 384 x 168 =
-// 256 x 208 + 128 x 88):
-//   warps 0..3, 4..7  softmax of the tile's rows 0..127 and 128..255 (one row per thread, so that no
-//                     shuffles are needed): S from TMEM, mask at the edges, P as BF16 back into the columns
-//                     of S; also Q into shared memory at the start and O out at the end
-//   warp 8            TMA: K and V tiles page by page (one box of 64 channels per page, at most 128 rows),
-//                     128-byte swizzle, two stages each
-//   warp 9            tcgen05.mma: S_a, S_b; then per cache tile P_a V, next S_a, P_b V, next S_b, so that one half's
-//                     products run under the other half's softmax; P is the A operand from TMEM, taken in two
-//                     halves of 64 keys as the softmax finishes them
-//   warp 10           zeros in the V rows of edge tiles that no row of the CTA sees
+// Warps (the softmax warps take registers that the last four give up, as setmaxnreg's comment there says):
+//   softmax     four per 128 rows, one row per thread, so that no shuffles are needed: S from TMEM, mask at the edges, P as
+//               BF16 back into TMEM; also Q into shared memory at the start and O out at the end
+//   TMA         K and V page by page (one box of 64 channels per page, at most 128 rows), 128-byte swizzle, two stages; V of a
+//               tile and K of the next share a barrier
+//   MMA         tcgen05.mma, P as the A operand from TMEM, taken in two halves of 64 keys as the softmax finishes them. At
+//               D = 128 two halves of rows alternate: P_a V, next S_a, P_b V, next S_b, so that one half's products run under
+//               the other's softmax, and P lies over its S (TMEM columns: S_a 0, S_b 128, O_a 256, O_b 384). At D = 64 a
+//               CTA has one half and two CTAs share an SM; P has columns of its own (S 0, O 128, P 192), so that the
+//               next S is formed as soon as this one is in registers.
+//   zeros       in the V rows of edge tiles that no row of the CTA sees
 // O is rescaled only when a row's maximum has grown by more than 2^8 since its reference was set (P then
-// stays below 2^8, harmless in BF16 and FP32); a commit of S_x(i) also covers P_x(i - 1) V, so O needs no barrier of its own.
-// TMEM columns: S_a 0, S_b 128, O_a 256, O_b 384. P is rounded to BF16 for the second product (half a
-// step, 2^-9 of each weight, below the BF16 output's own rounding); l sums the unrounded P.
+// stays below 2^8, harmless in BF16 and FP32). P is rounded to BF16 for the second product (at most 2^-9 of each weight);
+// l sums the unrounded P.
+// Where the tiles are fewer than the SMs, several CTAs share a walk and prefill_join_kernel adds their parts in order.
 //
 // Rows of a cache tile that no row of the CTA sees (past the last token, before the window, pages that
 // left the table) are not loaded where they fill a page, and their V rows are zeroed in shared memory: what
 // they hold cannot reach a result. Every wait is bounded; one that gives up latches KDA_ERR_TIMEOUT.
+//
+// Measured (BF16 1679 TFLOP/s in a burst, 1422 sustained): one prompt of 8192 tokens, 32 heads on 8 kv heads of 128, causal: 448 us =
+// 1227 TFLOP/s in a burst of 20, 527 us = 1043 once the power limit holds the clocks down; 4096 tokens 137 us; head_dim 64: 386 us.
+// A tile takes about 2950 cycles for 256 rows at D = 128 (a row half's chain: softmax 1840, its two products 1220) and 3180 at
+// D = 64, where two softmax warps per scheduler keep the exponential unit 60 % busy. Tried and slower: the row's keys
+// split between two threads (549 us: the maxima's exchange), a quarter to a half of the exponentials as polynomials on
+// the FMA pipe (no gain at 128, 398 to 474 us against 386 at 64: issue, not the unit, is short), S read twice from TMEM instead of kept in
+// registers (506), both halves' key halves with an O of their own at D = 64 (424), Q requested before the set-up's barrier (463: spills).
 #include <algorithm>
 #include <cmath>
 
@@ -349,6 +357,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp >= W) {
+      // 384 x 168 = 256 x 208 + 128 x 88 registers, or 256 x 128 = 128 x 200 + 128 x 56
       if constexpr (C::NH == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
       else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
       if (warp == W) {
