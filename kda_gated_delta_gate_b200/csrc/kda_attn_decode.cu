@@ -57,26 +57,27 @@ struct Span {
     int len, lo, sink, tiles;  // tiles = 0: the sequence is skipped
     int row0, n;               // its query rows
 };
+// What a sequence's span is made of, read without branches so that several sequences' reads can be in flight.
+struct Bounds {
+    int c0, c1, slot, len;  // len -1: the slot is none
+};
+__device__ __forceinline__ Bounds bounds_of(const DecodeArgs &a, int n) {
+    Bounds b;
+    b.slot = a.slots ? a.slots[n] : n;
+    b.c0 = a.cu ? a.cu[n] : n * a.K;
+    b.c1 = a.cu ? a.cu[n + 1] : n * a.K + a.K;
+    b.len = b.slot >= 0 && b.slot < a.c.max_seqs ? a.c.len[b.slot] : -1;
+    return b;
+}
 template <int kTile>
-__device__ __forceinline__ Span span_of(const DecodeArgs &a, int n, bool &bad) {
-    Span s{0, 0, 0, 0, n * a.K, a.K};
-    const int slot = a.slots ? a.slots[n] : n;
-    bad = true;
-    if (a.cu) {
-        const int c0 = a.cu[n], c1 = a.cu[n + 1];
-        if (c0 < 0 || c1 < c0 || c1 > a.total || c1 - c0 > a.K) return s;
-        s.row0 = c0;
-        s.n = c1 - c0;
-    }
-    if (slot < 0 || slot >= a.c.max_seqs) return s;
-    const int len = a.c.len[slot];
-    if (len < 0 || len > a.c.max_pages * a.c.page_size) return s;
-    bad = false;
-    if (s.n == 0) return s;
-    s.len = len;
-    s.lo = a.window ? max(0, len - s.n - a.window + 1) : 0;
+__device__ __forceinline__ Span span_of(const DecodeArgs &a, const Bounds &b, bool &bad) {
+    Span s{0, 0, 0, 0, b.c0, b.c1 - b.c0};
+    bad = b.c0 < 0 || b.c1 < b.c0 || b.c1 > a.total || b.c1 - b.c0 > a.K || b.len < 0 || b.len > a.c.max_pages * a.c.page_size;
+    if (bad || s.n == 0) return s;
+    s.len = b.len;
+    s.lo = a.window ? max(0, b.len - s.n - a.window + 1) : 0;
     if (s.lo > 0) s.sink = min((min(a.sinks, s.lo) + kTile - 1) / kTile, s.lo / kTile);
-    s.tiles = max(1, s.sink + (len + kTile - 1) / kTile - s.lo / kTile);  // an empty one still writes its zeros
+    s.tiles = max(1, s.sink + (b.len + kTile - 1) / kTile - s.lo / kTile);  // an empty one still writes its zeros
     return s;
 }
 template <int kTile>
@@ -416,10 +417,19 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, R>::CTAS) decode_kernel
     // ---- this CTA's run: the tiles of all sequences, summed by the whole block
     const int per = (a.N + kThreads - 1) / kThreads, n_lo = min(a.N, tid * per), n_hi = min(a.N, n_lo + per);
     long long mine = 0;
-    for (int n = n_lo; n < n_hi; ++n) {
-        bool bad;
-        mine += span_of<kTile>(a, n, bad).tiles;
-        if (bad && blockIdx.x == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+    for (int n0 = n_lo; n0 < n_hi; n0 += 4) {
+        Bounds bs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bs[k] = bounds_of(a, min(n0 + k, n_hi - 1));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            bool bad;
+            const int tiles = span_of<kTile>(a, bs[k], bad).tiles;
+            if (n0 + k < n_hi) {
+                mine += tiles;
+                if (bad && blockIdx.x == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+            }
+        }
     }
     mine *= hk;
     long long x = mine;
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, R>::CTAS) decode_kernel
         long long at = base;
         for (int n = n_lo; n < n_hi; ++n) {
             bool bad;
-            const long long w = static_cast<long long>(span_of<kTile>(a, n, bad).tiles) * hk;
+            const long long w = static_cast<long long>(span_of<kTile>(a, bounds_of(a, n), bad).tiles) * hk;
             if (t_begin < at + w) {
                 scur[0] = n;
                 scur[1] = at;
@@ -465,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<D, R>::CTAS) decode_kernel
     auto open = [&](Cursor &c) {  // the sequence's span; skips sequences without tiles
         bool bad;
         for (; c.n < a.N; ++c.n) {
-            c.s = span_of<kTile>(a, c.n, bad);
+            c.s = span_of<kTile>(a, bounds_of(a, c.n), bad);
             if (c.s.tiles > 0) break;
         }
         if (c.n < a.N) c.table = a.c.table + static_cast<size_t>(a.slots ? a.slots[c.n] : c.n) * a.c.max_pages;

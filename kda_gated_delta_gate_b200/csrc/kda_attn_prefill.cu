@@ -226,43 +226,46 @@ __device__ __forceinline__ bool has_dead_rows(const Tile &t, int i) {
     return i >= t.dead_from || i <= t.dead_to;
 }
 
-// Finds the row tile of `slot` (whole warps call): tiles of sequence b start at slot floor(bound(b) G / ROWS) + b, which
-// keeps them apart whatever the lengths; every lane looks at a sequence, so one round of reads does for 32. False:
-// no such tile, or its sequence is refused. `check`: look every sequence over and latch what is wrong.
+// Bounds of sequence b's rows, its slot and its length; false if one of them is none.
 __device__ __forceinline__ int row_bound(const PrefillArgs &a, int b) { return a.cu ? a.cu[b] : b * a.max_rows; }
+__device__ __forceinline__ bool sequence(const PrefillArgs &a, int b, int &c0, int &c1, int &slot, int &len) {
+    c0 = row_bound(a, b);
+    c1 = row_bound(a, b + 1);
+    slot = a.slots ? a.slots[b] : b;
+    len = slot >= 0 && slot < a.c.max_seqs ? a.c.len[slot] : -1;
+    return c0 >= 0 && c1 >= c0 && c1 <= a.total && c1 - c0 <= a.max_rows && len >= 0 && len <= a.c.max_pages * a.c.page_size;
+}
+
+// Finds the row tile of `slot` (whole warps call): tiles of sequence b start at slot floor(bound(b) G / ROWS) + b, which
+// keeps them apart whatever the lengths. Every lane looks at a sequence, so one round of reads does for 32 of them;
+// beyond that each round narrows the range 32 times first. False: no such tile, or its sequence is refused.
 template <int ROWS>
-__device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, bool check, Tile &t) {
+__device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, Tile &t) {
     auto first_slot = [&](int b, int c) { return static_cast<long long>(c) * a.G / ROWS + b; };
     const int lane = threadIdx.x & 31;
-    t.b = -1;
-    for (int b0 = 0; b0 < a.B && (t.b < 0 || check); b0 += 32) {
-        const int b = b0 + lane;
-        int c0 = 0, c1 = 0, s = -1, len = -1;
-        if (b < a.B) {
-            c0 = row_bound(a, b);
-            c1 = row_bound(a, b + 1);
-            s = a.slots ? a.slots[b] : b;
-            if (s >= 0 && s < a.c.max_seqs) len = a.c.len[s];
-        }
-        const bool ok = c0 >= 0 && c1 >= c0 && c1 <= a.total && c1 - c0 <= a.max_rows && len >= 0 &&
-                        len <= a.c.max_pages * a.c.page_size;
-        if (check && b < a.B && !ok) atomicExch(a.status, KDA_ERR_INVALID_ARG);
-        const bool here = b < a.B && first_slot(b, c0) <= slot && slot < first_slot(b + 1, c1);
-        const uint32_t hit = __ballot_sync(0xffffffffu, here);
-        if (hit && t.b < 0) {
-            const int src = __ffs(hit) - 1;
-            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, src)) {
-                t.b = a.B;  // found, and refused
-                continue;
-            }
-            t.b = b0 + src;
-            t.c0 = __shfl_sync(0xffffffffu, c0, src);
-            t.n = __shfl_sync(0xffffffffu, c1, src) - t.c0;
-            t.slot = __shfl_sync(0xffffffffu, s, src);
-            t.len = __shfl_sync(0xffffffffu, len, src);
-        }
+    int lo = 0, hi = a.B;
+    while (hi - lo > 32) {
+        const int step = (hi - lo + 31) / 32, b = lo + lane * step;
+        const uint32_t at_or_before = __ballot_sync(0xffffffffu, b < hi && first_slot(b, row_bound(a, b)) <= slot);
+        if (!at_or_before) return false;
+        lo += (31 - __clz(at_or_before)) * step;
+        hi = min(hi, lo + step);
     }
-    if (t.b < 0 || t.b >= a.B) return false;
+    int c0 = 0, c1 = 0, s = 0, len = 0;
+    bool ok = false, here = false;
+    if (lo + lane < hi) {
+        ok = sequence(a, lo + lane, c0, c1, s, len);
+        here = first_slot(lo + lane, c0) <= slot && slot < first_slot(lo + lane + 1, c1);
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, here);
+    if (!hit) return false;
+    const int src = __ffs(hit) - 1;
+    if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, src)) return false;
+    t.b = lo + src;
+    t.c0 = __shfl_sync(0xffffffffu, c0, src);
+    t.n = __shfl_sync(0xffffffffu, c1, src) - t.c0;
+    t.slot = __shfl_sync(0xffffffffu, s, src);
+    t.len = __shfl_sync(0xffffffffu, len, src);
     const long long r0 = (slot - first_slot(t.b, t.c0)) * ROWS, all_rows = static_cast<long long>(t.n) * a.G;
     if (r0 < 0 || r0 >= all_rows) return false;
     t.r0 = static_cast<int>(r0);
@@ -309,6 +312,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
     const int slot_id = a.nslots - 1 - static_cast<int>(blockIdx.x / a.splits / hk);  // the longest walks first
 
     // TMEM and barriers by two of the warps that do not compute, under every warp's search for the tile
+    if (warp == W + 3 && lane == 0 && blockIdx.x < static_cast<unsigned>(a.B)) {  // CTA b looks sequence b over
+        int c0, c1, s, len;
+        if (!sequence(a, blockIdx.x, c0, c1, s, len)) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+    }
     if (warp == W + 2 && lane == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&full[s], 1);
@@ -334,7 +341,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
     }
 
     Tile t;
-    const bool found = locate<C::ROWS>(a, slot_id, blockIdx.x == 0 && warp == 0, t);
+    const bool found = locate<C::ROWS>(a, slot_id, t);
     const int splits = found ? parts_of(a, t) : 0;
     if (split >= splits) {  // nothing to do here but to give the columns back
         __syncthreads();
@@ -676,7 +683,7 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
     grid_acquire();
     const int hk = a.c.kv_heads, h = blockIdx.x % hk, slot = blockIdx.x / hk, lane = threadIdx.x & 31;
     Tile t;
-    if (!locate<R>(a, slot, false, t)) return;
+    if (!locate<R>(a, slot, t)) return;
     const int splits = parts_of(a, t);
     if (splits == 1) return;
     const float *const ml = a.part_ml + 2 * (static_cast<size_t>(slot) * hk + h) * a.splits * R;

@@ -364,14 +364,27 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const KvView c, 
         }
     };
     request(tid);
-    // the sequence of every row: thread b marks its own (the first, should bounds overlap)
-    for (int b = tid; b < B; b += kAppendThreads) {
-        const int c0 = cu[b], c1 = cu[b + 1];
-        if (c0 < 0 || c1 < c0 || c1 > total || c1 > end) {
-            if (blockIdx.x == 0) atomicExch(status, KDA_ERR_INVALID_ARG);
-            continue;
+    // the sequence of every row: thread b marks its own; beyond a few rounds of that, a bisection per row
+    auto bounds = [&](int b, int &c0, int &c1) {
+        c0 = cu[b];
+        c1 = cu[b + 1];
+        return c0 >= 0 && c1 >= c0 && c1 <= total && c1 <= end;
+    };
+    int c0, c1;
+    for (int b = blockIdx.x * kAppendThreads + tid; b < B; b += gridDim.x * kAppendThreads)
+        if (!bounds(b, c0, c1)) atomicExch(status, KDA_ERR_INVALID_ARG);
+    if (B <= 4 * kAppendThreads) {
+        for (int b = tid; b < B; b += kAppendThreads)
+            if (bounds(b, c0, c1))
+                for (int r = max(c0 - row0, 0); r < min(c1 - row0, rows); ++r) atomicMin(&seq[r], b);
+    } else if (tid < rows && row0 + tid < end) {
+        int lo = 0, hi = B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid] <= row0 + tid) lo = mid;
+            else hi = mid;
         }
-        for (int r = max(c0 - row0, 0); r < min(c1 - row0, rows); ++r) atomicMin(&seq[r], b);
+        if (bounds(lo, c0, c1) && c0 <= row0 + tid && row0 + tid < c1) seq[tid] = lo;
     }
     __syncthreads();
     if (tid < rows) {

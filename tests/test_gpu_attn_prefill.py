@@ -74,6 +74,22 @@ def test_long_prompt():
     check(one, l1, (o[-1:], l[-1:], sp[-1:]))
 
 
+def test_many_sequences():
+    """More sequences than one round of a warp looks at, in both forms."""
+    rows = [(i * 5) % 4 for i in range(1100)]
+    rows[700] = 40
+    c = Case([r + (i * 3) % 50 for i, r in enumerate(rows)], rows, 2, 1, 64, 16, seed=5)
+    check(*run(c), c.expected())
+    out, lse = run(c, max_rows=40)
+    c.cache.seq_len[1000] = -1
+    again = run(c, max_rows=40)
+    assert kda.device_status(clear=True) == 1
+    hit = slice(c.cu[1000], c.cu[1001])
+    assert torch.isnan(again[0][hit]).all() and torch.equal(torch.nan_to_num(again[0], 9.0)[:hit.start], out[:hit.start])
+    few = Case([r + 20 for r in rows[:600]], rows[:600], 2, 1, 64, 16, seed=6)
+    check(*run(few), few.expected())
+
+
 def test_layers_slots_and_optional_arguments():
     c = Case([70, 130, 33], [20, 130, 3], 4, 2, 64, 16, layers=3, layer=1, order=[2, 0, 2, 1], seed=4)
     c.total = c.cu[-1]

@@ -148,6 +148,18 @@ def test_append_with_decreasing_bounds_writes_nothing_it_has_not_read():
     assert kda.device_status(clear=True) == 1 and torch.equal(p.cache.k, before)
 
 
+def test_append_of_many_sequences():
+    """More sequences than the rows' blocks mark one by one, empty ones among them."""
+    n = 1500
+    p = Pair(pages=n + 40, page=16, heads=1, seqs=n, max_pages=2, layers=1)
+    rows = [(i * 7) % 3 for i in range(n)]
+    kda.kda_kv_reserve(p.cache, None, _i32(rows), n)
+    p.model.reserve(range(n), rows)
+    p.append(0, list(range(n)), rows, ids=False)
+    order = [int(x) for x in np.random.default_rng(3).permutation(n)]
+    p.append(0, order, [rows[i] for i in order])
+
+
 def test_large_pools_and_many_slots():
     """More pages than one round of the scan, more pairs than one block has threads, far offsets: pages
     past the 2^32nd byte of a pool."""
