@@ -589,7 +589,7 @@ class KVCache:
         self.struct = KdaKvCache(_p(k), _p(v), _p(page_table), _p(seq_len), _p(ref), _p(self.scratch),
                                  k.stride(0) if layers > 1 else k[0].numel() if layers else 0, layers, num_pages,
                                  page_size, kv_heads, head_dim, max_seqs, max_pages)
-        self._torch, self._device = torch, k.device.index
+        self._torch, self._device, self._dev = torch, k.device.index, k.device
         self._width = kv_heads * head_dim
         self._ref = ctypes.byref(self.struct)
         self._need = {}  # scratch bytes of the attention calls by their sizes
@@ -617,56 +617,59 @@ def _on(cache: KVCache, stream):
     return cache._ref, _raw_stream(dev)
 
 
-def _ints(cache: KVCache, *ts):
-    """Device pointers of int32 arrays (None stays NULL)."""
-    int32 = cache._torch.int32
+def _ints(cache: KVCache, *ts, n: int = 0):
+    """Device pointers of int32 arrays of at least n entries (None stays NULL)."""
+    int32, dev = cache._torch.int32, cache._dev
     for t in ts:
-        if t is not None and (t.dtype is not int32 or not t.is_contiguous()):
-            raise ValueError(f"index arrays are contiguous int32 tensors, not {t.dtype}")
+        if t is not None and (t.dtype is not int32 or not t.is_contiguous() or t.numel() < n or t.device != dev):
+            raise ValueError(f"index arrays are contiguous int32 tensors of at least {n} entries on {cache.k.device}, not "
+                             f"{t.numel()} of {t.dtype} on {t.device}")
     return [_p(t) for t in ts]
 
 
 def _attn_rows(cache: KVCache, rows: int, d: KdaDims, q, out, lse):
     """Pointers of q, out and lse after a look at their types and sizes."""
-    n, torch = rows * d.heads, cache._torch
+    n, torch, dev = rows * d.heads, cache._torch, cache._dev
     size = n * d.head_dim
     for name, t, dt, size in (("q", q, torch.bfloat16, size), ("out", out, torch.bfloat16, size),
                               ("lse", lse, torch.float32, n)):
-        if t is not None and (t.dtype is not dt or not t.is_contiguous() or t.numel() < size):
-            raise ValueError(f"{name} is a contiguous {dt} tensor of at least {size} values")
+        if t is not None and (t.dtype is not dt or not t.is_contiguous() or t.numel() < size or t.device != dev):
+            raise ValueError(f"{name} is a contiguous {dt} tensor of at least {size} values on {cache.k.device}")
     return _p(q), _p(out), _p(lse)
 
 
 def kda_kv_reserve(cache: KVCache, slots, add, n: int, stream=None):
     """Room for add[i] more tokens in slot slots[i] (device int32 [n]; slots None: slot i)."""
     ref, st = _on(cache, stream)
-    return _call("kda_kv_reserve", ref, *_ints(cache, slots, add), n, st)
+    return _call("kda_kv_reserve", ref, *_ints(cache, slots, add, n=n), n, st)
 
 
 def kda_kv_fork(cache: KVCache, parent, child, n: int, stream=None):
     """Slot child[i] becomes a copy of slot parent[i]: full pages shared, a partly filled last page copied."""
     ref, st = _on(cache, stream)
-    return _call("kda_kv_fork", ref, *_ints(cache, parent, child), n, st)
+    return _call("kda_kv_fork", ref, *_ints(cache, parent, child, n=n), n, st)
 
 
 def kda_kv_truncate(cache: KVCache, slots, new_len, n: int, stream=None):
     """Slot slots[i] keeps its first new_len[i] tokens (0 frees it)."""
     ref, st = _on(cache, stream)
-    return _call("kda_kv_truncate", ref, *_ints(cache, slots, new_len), n, st)
+    return _call("kda_kv_truncate", ref, *_ints(cache, slots, new_len, n=n), n, st)
 
 
 def kda_kv_compact(cache: KVCache, live=None, stream=None):
     """Move the live pages to the front of the pools; live (device int32 [1]) receives their number."""
     ref, st = _on(cache, stream)
-    return _call("kda_kv_compact", ref, *_ints(cache, live), st)
+    return _call("kda_kv_compact", ref, *_ints(cache, live, n=1), st)
 
 
 def _rows_stride(cache: KVCache, k_new, v_new, rows: int) -> int:
     """The row stride of k_new and v_new: BF16 rows [rows or more, kv_heads * head_dim] or [.., kv_heads, head_dim]
     of contiguous values, both of one shape and row stride."""
     w, bf16, size, step = cache._width, cache._torch.bfloat16, k_new.shape, k_new.stride()
-    if k_new.dtype is not bf16 or v_new.dtype is not bf16 or v_new.shape != size or size[0] < rows:
-        raise ValueError(f"k_new and v_new are bfloat16 tensors of one shape, at least {rows} rows of {w} values")
+    if (k_new.dtype is not bf16 or v_new.dtype is not bf16 or v_new.shape != size or size[0] < rows or
+            k_new.device != cache._dev or v_new.device != cache._dev):
+        raise ValueError(f"k_new and v_new are bfloat16 tensors of one shape on {cache.k.device}, at least {rows} rows of "
+                         f"{w} values")
     inner = step[1:]
     if not (len(size) == 2 and size[1] == w and inner == (1,) or
             len(size) == 3 and size[1] * size[2] == w and inner == (size[2], 1)) or v_new.stride()[1:] != inner:
@@ -684,8 +687,8 @@ def kda_kv_append(cache: KVCache, layer: int, k_new, v_new, cu_seqlens, slots, B
     stride) into the pages of their sequences, whose last tokens they are."""
     ref, st = _on(cache, stream)
     ld = _rows_stride(cache, k_new, v_new, total_tokens)
-    return _call("kda_kv_append", ref, layer, _p(k_new), _p(v_new), ld, *_ints(cache, cu_seqlens, slots), B,
-                 total_tokens, st)
+    return _call("kda_kv_append", ref, layer, _p(k_new), _p(v_new), ld,
+                 *_ints(cache, cu_seqlens, n=B + 1), *_ints(cache, slots, n=B), B, total_tokens, st)
 
 
 def kda_attn_decode_scratch_bytes(N: int, K: int, d: KdaDims, cache: KVCache) -> int:
@@ -716,8 +719,10 @@ def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d
     ref, st = _on(cache, stream)
     if scratch is None:
         scratch = _attn_scratch(kda_attn_decode_scratch_bytes, (N, K), d, cache, st)
+    elif scratch.device != cache._dev or not scratch.is_contiguous():
+        raise ValueError(f"scratch is a contiguous tensor on {cache.k.device}")
     pq, po, pl = _attn_rows(cache, N * K, d, q, out, lse)
-    return _call("kda_attn_decode", ref, layer, pq, *_ints(cache, slots), N, K, window, sinks, po,
+    return _call("kda_attn_decode", ref, layer, pq, *_ints(cache, slots, n=N), N, K, window, sinks, po,
                  pl, _p(scratch), scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
 
 
@@ -729,7 +734,9 @@ def kda_attn_prefill(cache: KVCache, layer: int, q, cu_seqlens, slots, B: int, m
     ref, st = _on(cache, stream)
     if scratch is None:
         scratch = _attn_scratch(kda_attn_prefill_scratch_bytes, (B, max_rows, total_tokens), d, cache, st)
+    elif scratch.device != cache._dev or not scratch.is_contiguous():
+        raise ValueError(f"scratch is a contiguous tensor on {cache.k.device}")
     pq, po, pl = _attn_rows(cache, total_tokens, d, q, out, lse)
-    return _call("kda_attn_prefill", ref, layer, pq, *_ints(cache, cu_seqlens, slots), B, max_rows,
-                 total_tokens, window, sinks, po, pl, _p(scratch), scratch.numel() * scratch.element_size(),
+    return _call("kda_attn_prefill", ref, layer, pq, *_ints(cache, cu_seqlens, n=B + 1), *_ints(cache, slots, n=B), B,
+                 max_rows, total_tokens, window, sinks, po, pl, _p(scratch), scratch.numel() * scratch.element_size(),
                  ctypes.byref(d), st)

@@ -150,3 +150,40 @@ def test_binding_checks_types_and_sizes():
     for t in (torch.zeros(2, dtype=torch.int64), torch.zeros(4, dtype=torch.int32)[::2]):
         with pytest.raises(ValueError):
             kda._ints(c, t)
+
+
+def test_calls_refuse_short_or_foreign_tensors(monkeypatch):
+    """Arrays with fewer entries than the call reads, and tensors on another device than the cache's."""
+    bf = lambda *shape, dev="cpu": torch.zeros(*shape, dtype=torch.bfloat16, device=dev)
+    ints = lambda n, dev="cpu": torch.zeros(n, dtype=torch.int32, device=dev)
+    d = kda.dims(4, 64)
+    c = kda.KVCache(bf(1, 4, 2, 16, 64), bf(1, 4, 2, 16, 64), ints(15).view(3, 5), ints(3), ints(4))
+    calls = []
+    monkeypatch.setattr(kda, "_on", lambda cache, stream: (cache._ref, 0))
+    monkeypatch.setattr(kda, "_call", lambda name, *args: calls.append(name))
+    q, scr = bf(4, 4, 64), torch.zeros(64, dtype=torch.uint8)
+    kda.kda_kv_reserve(c, ints(2), ints(2), 2)
+    kda.kda_kv_fork(c, ints(2), ints(2), 2)
+    kda.kda_kv_truncate(c, None, ints(2), 2)
+    kda.kda_kv_compact(c, ints(1))
+    kda.kda_kv_append(c, 0, bf(4, 128), bf(4, 128), ints(3), ints(2), 2, 4)
+    kda.kda_attn_decode(c, 0, q, ints(4), 4, 1, q.clone(), d, scratch=scr)
+    kda.kda_attn_prefill(c, 0, q, ints(3), ints(2), 2, 4, 4, q.clone(), d, scratch=scr)
+    assert len(calls) == 7
+    m = "meta"  # stands for another device
+    for bad in (lambda: kda.kda_kv_reserve(c, ints(1), ints(2), 2), lambda: kda.kda_kv_reserve(c, None, ints(1), 2),
+                lambda: kda.kda_kv_reserve(c, None, ints(2, m), 2),
+                lambda: kda.kda_kv_fork(c, ints(2), ints(1), 2), lambda: kda.kda_kv_fork(c, ints(2, m), ints(2), 2),
+                lambda: kda.kda_kv_truncate(c, ints(2), ints(1), 2), lambda: kda.kda_kv_compact(c, ints(0)),
+                lambda: kda.kda_kv_append(c, 0, bf(4, 128), bf(4, 128), ints(2), ints(2), 2, 4),
+                lambda: kda.kda_kv_append(c, 0, bf(4, 128), bf(4, 128), ints(3), ints(1), 2, 4),
+                lambda: kda.kda_kv_append(c, 0, bf(4, 128, dev=m), bf(4, 128, dev=m), ints(3), ints(2), 2, 4),
+                lambda: kda.kda_attn_decode(c, 0, q, ints(3), 4, 1, q.clone(), d, scratch=scr),
+                lambda: kda.kda_attn_decode(c, 0, bf(4, 4, 64, dev=m), None, 4, 1, q.clone(), d, scratch=scr),
+                lambda: kda.kda_attn_decode(c, 0, q, None, 4, 1, q.clone(), d, scratch=scr.to(m)),
+                lambda: kda.kda_attn_prefill(c, 0, q, ints(2), None, 2, 4, 4, q.clone(), d, scratch=scr),
+                lambda: kda.kda_attn_prefill(c, 0, q, ints(3), ints(1), 2, 4, 4, q.clone(), d, scratch=scr),
+                lambda: kda.kda_attn_prefill(c, 0, q, ints(3), None, 2, 4, 4, q.clone(), d, scratch=scr[::2])):
+        with pytest.raises(ValueError):
+            bad()
+    assert len(calls) == 7
