@@ -204,9 +204,18 @@ def scratch_buffer(nbytes: int, device, stream_handle: int):
     key = (dev.index if dev.index is not None else torch.cuda.current_device(), int(stream_handle))
     buf = _SCRATCH.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=dev)
-        _SCRATCH[key] = buf
+        buf = _SCRATCH[key] = _empty_on(max(int(nbytes), 16), key[0], key[1])
     return buf
+
+
+def _empty_on(nbytes: int, dev: int, stream_handle: int):
+    """nbytes bytes of stream `stream_handle`'s memory: what the allocator hands out, and what it takes back later, is then
+    ordered with that stream's work, also where the call's stream is not the current one."""
+    import torch
+    if torch.cuda.current_stream(dev).cuda_stream == stream_handle:
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream_handle, device=dev)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
 
 
 def device_status(clear: bool = True) -> int:
@@ -700,16 +709,23 @@ def kda_attn_prefill_scratch_bytes(B: int, max_rows: int, total_tokens: int, d: 
                                                     ctypes.byref(cache.struct)))
 
 
-def _attn_scratch(fn, key, d: KdaDims, cache: KVCache, stream_handle: int):
-    """The stream's cached buffer, of at least fn(*key) bytes; while the current stream is being captured a buffer of the
+def _attn_scratch(fn, key, d: KdaDims, cache: KVCache, stream, stream_handle: int):
+    """The stream's cached buffer, of at least fn(*key) bytes; while the stream is being captured a buffer of the
     graph's own, so that graphs captured one after the other may run at once."""
     torch = cache._torch
     need = cache._need.get((key, d.heads, d.head_dim))
     if need is None:
+        if len(cache._need) >= 4096:  # sizes that change from call to call are not kept for good
+            cache._need.clear()
         need = cache._need[key, d.heads, d.head_dim] = fn(*key, d, cache)
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.k.device)
-    return scratch_buffer(need, cache.k.device, stream_handle)
+    if stream is None or _stream(None) == stream_handle:
+        capturing = torch.cuda.is_current_stream_capturing()
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream_handle, device=cache._dev)):
+            capturing = torch.cuda.is_current_stream_capturing()
+    if capturing:
+        return _empty_on(max(need, 16), cache._device, stream_handle)
+    return scratch_buffer(need, cache._dev, stream_handle)
 
 
 def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d: KdaDims, window: int = 0,
@@ -718,7 +734,7 @@ def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d
     lse [N*K, heads] F32 or None). `scratch`: kda_attn_decode_scratch_bytes bytes; a cached buffer when None."""
     ref, st = _on(cache, stream)
     if scratch is None:
-        scratch = _attn_scratch(kda_attn_decode_scratch_bytes, (N, K), d, cache, st)
+        scratch = _attn_scratch(kda_attn_decode_scratch_bytes, (N, K), d, cache, stream, st)
     elif scratch.device != cache._dev or not scratch.is_contiguous():
         raise ValueError(f"scratch is a contiguous tensor on {cache.k.device}")
     pq, po, pl = _attn_rows(cache, N * K, d, q, out, lse)
@@ -733,7 +749,7 @@ def kda_attn_prefill(cache: KVCache, layer: int, q, cu_seqlens, slots, B: int, m
     kda_attn_decode (kda_attn_prefill_scratch_bytes)."""
     ref, st = _on(cache, stream)
     if scratch is None:
-        scratch = _attn_scratch(kda_attn_prefill_scratch_bytes, (B, max_rows, total_tokens), d, cache, st)
+        scratch = _attn_scratch(kda_attn_prefill_scratch_bytes, (B, max_rows, total_tokens), d, cache, stream, st)
     elif scratch.device != cache._dev or not scratch.is_contiguous():
         raise ValueError(f"scratch is a contiguous tensor on {cache.k.device}")
     pq, po, pl = _attn_rows(cache, total_tokens, d, q, out, lse)

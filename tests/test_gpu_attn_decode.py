@@ -187,3 +187,52 @@ def test_calls_on_another_device_are_refused(monkeypatch):
                  lambda: kda.kda_kv_append(c.cache, 0, c.qd[:, :2], c.qd[:, 2:], i32([0, 1]), None, 1, 1, stream=0)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_scratch_belongs_to_the_stream_of_the_call():
+    """Scratch for an explicit stream is not memory that the current stream has just given back with work still queued on it."""
+    side = torch.cuda.Stream()
+    n = 48 << 20
+    freed = torch.empty(n, dtype=torch.uint8, device="cuda")
+    at = freed.data_ptr()
+    del freed
+    buf = kda.scratch_buffer(n, "cuda", side.cuda_stream)
+    assert buf.data_ptr() != at and buf.numel() >= n
+    again = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert again.data_ptr() == at  # the freed block was there to be had
+    assert kda.scratch_buffer(n, "cuda", side.cuda_stream) is buf
+    kda._SCRATCH.pop((torch.cuda.current_device(), side.cuda_stream))
+
+
+def test_an_explicit_stream_and_its_capture():
+    """Calls on another stream than the current one, eager and captured on a branch of a graph beside one on the trunk."""
+    cs = [Case([900, 31, 2000], [1] * 3, 8, 2, 128, 16, seed=s) for s in (11, 12)]
+    want = [c.expected() for c in cs]
+    side = torch.cuda.Stream()
+    outs = [(torch.empty_like(c.qd), torch.empty((3, 8), device="cuda")) for c in cs]
+    slots = [i32(c.order) for c in cs]
+    torch.cuda.synchronize()
+
+    def call(i, stream=None):
+        kda.kda_attn_decode(cs[i].cache, 0, cs[i].qd, slots[i], 3, 1, outs[i][0], cs[i].d, lse=outs[i][1], stream=stream)
+
+    call(0)
+    call(1, side)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        check(*o, w)
+        o[0].zero_(), o[1].zero_()
+    g, fork, join = torch.cuda.CUDAGraph(), torch.cuda.Event(), torch.cuda.Event()
+    with torch.cuda.graph(g):
+        trunk = torch.cuda.current_stream()
+        fork.record(trunk)
+        side.wait_event(fork)
+        call(1, side)
+        call(0)
+        join.record(side)
+        trunk.wait_event(join)
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        check(*o, w)
