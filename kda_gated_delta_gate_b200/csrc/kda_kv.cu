@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kBookThreads) take_pages_kernel(const KvView c
     // `wide` threads per pair, so that few pairs of many pages and many pairs of few both take few rounds; refs and
     // lengths have all been read by now
     int wide = kBookThreads;
-    while (wide > 4 && wide * n > kBookThreads) wide >>= 1;
+    while (wide > 4 && n > kBookThreads / wide) wide >>= 1;
     const int lane = tid & (wide - 1);
     for (int i = tid / wide; i < n; i += kBookThreads / wide) {
         int first = b.first[i];
