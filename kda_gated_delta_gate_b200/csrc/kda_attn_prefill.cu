@@ -505,10 +505,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             gone ^= 1u << (i & 1);
             if (!wait_or_abort(&full[i & 1], (i >> 1) & 1, abort, a.status)) break;
             const int j0 = tile_row0(t, i);
+            // a row is 128 bytes of each 64-channel half, in whatever order the swizzle keeps them
+            const int hi = t.hi - j0, lo = t.lo - j0, sinks = a.sinks - j0;
             for (int e = lane; e < kKeys * (D / 8); e += 32) {
-                const int r = e / (D / 8), c = e % (D / 8), j = j0 + r;
-                if (j >= t.hi || (j < t.lo && j >= a.sinks))
-                    *reinterpret_cast<uint4 *>(sv + kmaj_off(r, 8 * c, kKeys)) = make_uint4(0u, 0u, 0u, 0u);
+                const int r = e / 8 % kKeys;
+                if (r >= hi || (r < lo && r >= sinks)) *reinterpret_cast<uint4 *>(sv + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_async_smem();
             __syncwarp();
@@ -524,17 +525,22 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
         const int tok = (t.r0 + r) / a.G, g = t.r0 + r - tok * a.G;
         const size_t row = static_cast<size_t>(t.c0 + (real ? tok : 0)) * a.heads + static_cast<size_t>(h) * a.G + (real ? g : 0);
         const int pos = t.base + min(tok, t.n - 1);
+        constexpr int LR = D / 8, RP = 32 / LR;  // lanes per row and rows per pass of Q's and O's copies
         {
-            const uint4 *const src = reinterpret_cast<const uint4 *>(a.q + row * D);
-            uint8_t *const dst = sm + x * C::TILE;
+            uint8_t *const rows_sm = sm + x * C::TILE + 32 * (warp & 3) * 128;
+            const uint32_t reals = __ballot_sync(0xffffffffu, real);
+            // D / 8 lanes bring a row: 5700 cycles from here to the barrier where every lane brought its own, 1500 so
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 v = real ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < LR; ++k) {
+                const int of = RP * k + lane / LR;
+                const size_t from = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(row), of);
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (reals >> of & 1u) v = __ldg(reinterpret_cast<const uint4 *>(a.q + from * D) + lane % LR);
                 v.x ^= a.flip;
                 v.y ^= a.flip;
                 v.z ^= a.flip;
                 v.w ^= a.flip;
-                *reinterpret_cast<uint4 *>(dst + kmaj_off(r & 127, 8 * c, 128)) = v;
+                *reinterpret_cast<uint4 *>(rows_sm + kmaj_off(of, 8 * (lane % LR), 128)) = v;
             }
             fence_async_smem();
             __syncwarp();
@@ -648,23 +654,33 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             if (*bad_page && tid == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
         } else if (ok && !*bad_page) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint4 *const dst = reinterpret_cast<uint4 *>(a.out + row * D);
+            uint8_t *const rows_sm = sm + x * C::TILE + 32 * (warp & 3) * 128;  // Q has been read
+            int ln = lane;  // hidden from the compiler, which would keep the addresses of Q's copy in registers for this one
+            asm volatile("" : "+r"(ln));
+            const uint32_t reals = __ballot_sync(0xffffffffu, real);
 #pragma unroll
-            for (int c = 0; c < D; c += 16) {
-                float o[16];
-                tmem_ld16(to + c, o);
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(to + c, o);
                 tmem_ld_wait();
                 if (tiles == 0 || l == 0.f) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
                 }
-                uint32_t u[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
-                if (real) {
-                    dst[c / 8] = make_uint4(u[0], u[1], u[2], u[3]);
-                    dst[c / 8 + 1] = make_uint4(u[4], u[5], u[6], u[7]);
-                }
+                for (int e = 0; e < 32; e += 8)
+                    *reinterpret_cast<uint4 *>(rows_sm + kmaj_off(ln, c + e, 128)) =
+                        make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                   pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < LR; ++k) {
+                const int of = RP * k + ln / LR;
+                const size_t at = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(row), of);
+                if (reals >> of & 1u)
+                    *(reinterpret_cast<uint4 *>(a.out + at * D) + ln % LR) =
+                        *reinterpret_cast<const uint4 *>(rows_sm + kmaj_off(of, 8 * (ln % LR), 128));
             }
             if (a.lse && real) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         } else if (*bad_page && tid == 0) {
