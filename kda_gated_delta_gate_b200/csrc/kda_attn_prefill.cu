@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
         {
             uint8_t *const rows_sm = sm + x * C::TILE + 32 * (warp & 3) * 128;
             const uint32_t reals = __ballot_sync(0xffffffffu, real);
-            // D / 8 lanes bring a row: 5700 cycles from here to the barrier where every lane brought its own, 1500 so
+            // D / 8 lanes bring a row: 3100 cycles at head_dim 128; where every lane brought its own, 5700
 #pragma unroll
             for (int k = 0; k < LR; ++k) {
                 const int of = RP * k + lane / LR;
@@ -652,12 +652,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             }
             *reinterpret_cast<float2 *>(a.part_ml + 2 * pr) = make_float2(m, ok && !*bad_page ? l : -1.f);
             if (*bad_page && tid == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
-        } else if (ok && !*bad_page) {
+        } else if (__all_sync(0xffffffffu, ok && !*bad_page)) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
             uint8_t *const rows_sm = sm + x * C::TILE + 32 * (warp & 3) * 128;  // Q has been read
             int ln = lane;  // hidden from the compiler, which would keep the addresses of Q's copy in registers for this one
             asm volatile("" : "+r"(ln));
-            const uint32_t reals = __ballot_sync(0xffffffffu, real);
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -668,19 +667,26 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
                     for (int e = 0; e < 32; ++e) o[e] = 0.f;
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    *reinterpret_cast<uint4 *>(rows_sm + kmaj_off(ln, c + e, 128)) =
-                        make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                                   pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+                for (int e = 0; e < 32; e += 8) {
+                    const uint4 u = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                               pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+                    if (D == 128) *reinterpret_cast<uint4 *>(rows_sm + kmaj_off(ln, c + e, 128)) = u;
+                    else if (real) *reinterpret_cast<uint4 *>(a.out + row * D + c + e) = u;
+                }
             }
-            __syncwarp();
+            // whole rows at a time through shared memory (8192 rows x 32 heads: 452 us with Q and O by own rows, 441 so); at
+            // head_dim 64 a row is one 128-byte line, and a lane writes its own (387 us against 389)
+            if (D == 128) {
+                const uint32_t reals = __ballot_sync(0xffffffffu, real);
+                __syncwarp();
 #pragma unroll
-            for (int k = 0; k < LR; ++k) {
-                const int of = RP * k + ln / LR;
-                const size_t at = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(row), of);
-                if (reals >> of & 1u)
-                    *(reinterpret_cast<uint4 *>(a.out + at * D) + ln % LR) =
-                        *reinterpret_cast<const uint4 *>(rows_sm + kmaj_off(of, 8 * (ln % LR), 128));
+                for (int k = 0; k < LR; ++k) {
+                    const int of = RP * k + ln / LR;
+                    const size_t at = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(row), of);
+                    if (reals >> of & 1u)
+                        *(reinterpret_cast<uint4 *>(a.out + at * D) + ln % LR) =
+                            *reinterpret_cast<const uint4 *>(rows_sm + kmaj_off(of, 8 * (ln % LR), 128));
+                }
             }
             if (a.lse && real) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         } else if (*bad_page && tid == 0) {
