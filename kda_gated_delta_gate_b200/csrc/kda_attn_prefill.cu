@@ -679,13 +679,14 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             if (D == 128) {
                 const uint32_t reals = __ballot_sync(0xffffffffu, real);
                 __syncwarp();
+                uint4 v[LR];
+#pragma unroll
+                for (int k = 0; k < LR; ++k)
+                    v[k] = *reinterpret_cast<const uint4 *>(rows_sm + kmaj_off(RP * k + ln / LR, 8 * (ln % LR), 128));
 #pragma unroll
                 for (int k = 0; k < LR; ++k) {
-                    const int of = RP * k + ln / LR;
-                    const size_t at = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(row), of);
-                    if (reals >> of & 1u)
-                        *(reinterpret_cast<uint4 *>(a.out + at * D) + ln % LR) =
-                            *reinterpret_cast<const uint4 *>(rows_sm + kmaj_off(of, 8 * (ln % LR), 128));
+                    const size_t at = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(row), RP * k + ln / LR);
+                    if (reals >> (RP * k + ln / LR) & 1u) *(reinterpret_cast<uint4 *>(a.out + at * D) + ln % LR) = v[k];
                 }
             }
             if (a.lse && real) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
