@@ -26,13 +26,19 @@
 // left the table) are not loaded where they fill a page, and their V rows are zeroed in shared memory: what
 // they hold cannot reach a result. Every wait is bounded; one that gives up latches KDA_ERR_TIMEOUT.
 //
-// Measured (BF16 1679 TFLOP/s in a burst, 1422 sustained): one prompt of 8192 tokens, 32 heads on 8 kv heads of 128, causal: 448 us =
-// 1227 TFLOP/s in a burst of 20, 527 us = 1043 once the power limit holds the clocks down; 4096 tokens 137 us; head_dim 64: 386 us.
+// Measured (BF16 1679 TFLOP/s in a burst, 1422 sustained): one prompt of 8192 tokens, 32 heads on 8 kv heads of 128, causal: 438 us =
+// 1255 TFLOP/s in a burst of 20, 500 us = 1099 once the power limit holds the clocks down; 4096 tokens 127 us, 2048 44;
+// head_dim 64: 387 us.
 // A tile takes about 2950 cycles for 256 rows at D = 128 (a row half's chain: softmax 1840, its two products 1220) and 3180 at
-// D = 64, where two softmax warps per scheduler keep the exponential unit 60 % busy. Tried and slower: the row's keys
+// D = 64, where two softmax warps per scheduler keep the exponential unit 60 % busy. Before its first tile a CTA spends 6500 cycles
+// (bounds, slot, length and page entry, which depend on one another; Q; K) and after its last product 3000 on O; nothing runs
+// under these at D = 128. Tried and slower: the row's keys
 // split between two threads (549 us: the maxima's exchange), a quarter to a half of the exponentials as polynomials on
 // the FMA pipe (no gain at 128, 398 to 474 us against 386 at 64: issue, not the unit, is short), S read twice from TMEM instead of kept in
-// registers (506), both halves' key halves with an O of their own at D = 64 (424), Q requested before the set-up's barrier (463: spills).
+// registers (506), both halves' key halves with an O of their own at D = 64 (424), Q requested before the set-up's barrier (463: spills;
+// later, with Q by whole rows and K of tile 0 too, 451 against 447), CTAs that take further tiles in place by cluster launch
+// control, the next tile's K and Q loaded under this one's end (438 against 434, 397 against 388 at 64: what it saves between tiles,
+// 3 to 5 %, the products' loop loses to stages that no longer are constants), 200 + 104 registers for 208 + 88 (449 against 446).
 #include <algorithm>
 #include <cmath>
 
