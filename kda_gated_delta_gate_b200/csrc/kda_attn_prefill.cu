@@ -242,12 +242,14 @@ __device__ __forceinline__ bool sequence(const PrefillArgs &a, int b, int &c0, i
     return c0 >= 0 && c1 >= c0 && c1 <= a.total && c1 - c0 <= a.max_rows && len >= 0 && len <= a.c.max_pages * a.c.page_size;
 }
 
-// Finds the row tile of `slot` (whole warps call): tiles of sequence b start at slot floor(bound(b) G / ROWS) + b, which
-// keeps them apart whatever the lengths. Every lane looks at a sequence, so one round of reads does for 32 of them;
+// Finds the row tile of `slot` (whole warps call): tiles of sequence b start at slot floor(c G / ROWS) + min(b, c), c its
+// first row. The next sequence with rows has a larger b and a larger c, so that its slot is at least one past what the floors
+// differ by, which keeps the tiles apart whatever the lengths; sequences without rows take no slots once there are
+// more of them than rows before them. Every lane looks at a sequence, so one round of reads does for 32 of them;
 // beyond that each round narrows the range 32 times first. False: no such tile, or its sequence is refused.
 template <int ROWS>
 __device__ __forceinline__ bool locate(const PrefillArgs &a, int slot, Tile &t) {
-    auto first_slot = [&](int b, int c) { return static_cast<long long>(c) * a.G / ROWS + b; };
+    auto first_slot = [&](int b, int c) { return static_cast<long long>(c) * a.G / ROWS + min(b, c); };
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = a.B;
     while (hi - lo > 32) {
@@ -318,9 +320,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
     const int slot_id = a.nslots - 1 - static_cast<int>(blockIdx.x / a.splits / hk);  // the longest walks first
 
     // TMEM and barriers by two of the warps that do not compute, under every warp's search for the tile
-    if (warp == W + 3 && lane == 0 && blockIdx.x < static_cast<unsigned>(a.B)) {  // CTA b looks sequence b over
-        int c0, c1, s, len;
-        if (!sequence(a, blockIdx.x, c0, c1, s, len)) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+    if (warp == W + 3) {  // CTA b looks sequence b over, and where there are fewer CTAs its other lanes those further on
+        for (long long b = blockIdx.x + static_cast<long long>(lane) * gridDim.x; b < a.B; b += 32LL * gridDim.x) {
+            int c0, c1, s, len;
+            if (!sequence(a, static_cast<int>(b), c0, c1, s, len)) atomicExch(a.status, KDA_ERR_INVALID_ARG);
+        }
     }
     if (warp == W + 2 && lane == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -794,7 +798,10 @@ int launch_prefill(const PrefillArgs &a, unsigned grid, cudaStream_t s) {
 namespace kda {
 
 namespace {
-long long tile_slots(int B, int total, int G, int D) { return static_cast<long long>(total) * G / tile_rows(D) + B; }
+// Slots of row tiles (see locate): no more than twice what total rows need, however many sequences have none
+long long tile_slots(int B, int total, int G, int D) {
+    return static_cast<long long>(total) * G / tile_rows(D) + std::min(B, total);
+}
 }  // namespace
 
 bool attn_tiles_fits(int B, int total, int heads, const kda_kv_cache *cache) {

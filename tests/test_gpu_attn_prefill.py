@@ -286,3 +286,20 @@ def test_serving_run():
     step([5, 2, 3], [30, 61, 2], window=40, sinks=3)
     step([5, 2, 3], [1, 1, 1], prefill=False, window=40, sinks=3)
     assert cache.seq_len.tolist() == [len(host[s][0]) for s in range(6)]
+
+
+@pytest.mark.parametrize("B,busy,heads,kv_heads,dim", [(2000, {3: (2100, 3), 1998: (700, 2)}, 32, 2, 128),
+                                                       (300, {0: (900, 140), 150: (40, 1), 299: (1300, 60)}, 4, 1, 64),
+                                                       (70, {64: (600, 1)}, 33, 1, 64)])
+def test_few_sequences_with_rows_among_many_without(B, busy, heads, kv_heads, dim):
+    """A fixed list of slots, most of them without rows: fewer row tiles than sequences, walks shared by several CTAs."""
+    lens, rows = [i % 3 for i in range(B)], [0] * B
+    for s, (n, r) in busy.items():
+        lens[s], rows[s] = n, r
+    c = Case(lens, rows, heads, kv_heads, dim, 16, seed=B)
+    out, lse = run(c)
+    check(out, lse, c.expected())
+    c.cache.seq_len[B - 2 if B - 2 not in busy else B - 3] = -1  # one without rows that is refused all the same
+    again = run(c)
+    assert kda.device_status(clear=True) == 1
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])

@@ -187,3 +187,15 @@ def test_calls_refuse_short_or_foreign_tensors(monkeypatch):
         with pytest.raises(ValueError):
             bad()
     assert len(calls) == 7
+
+
+@pytest.mark.parametrize("B,rows,total,heads,kv_heads,dim", [(256, 1, 1, 64, 1, 128), (1024, 2, 2, 64, 1, 128), (4096, 3, 3, 16, 1, 128),
+                                                             (65535, 40, 40, 1, 1, 64), (300, 9, 700, 48, 8, 64), (65535, 7, 900, 32, 2, 128)])
+def test_scratch_does_not_grow_with_sequences_without_rows(L, B, rows, total, heads, kv_heads, dim):
+    """Parts are kept for at most twice the tiles that can hold rows, and these with their splits fill the SMs once:
+    148 CTAs of 256 rows at head_dim 128, 296 of 128 rows at 64, (dim + 4) FP32 values a row."""
+    c = _c(num_pages=1 << 14, page_size=64, kv_heads=kv_heads, head_dim=dim, max_seqs=65536, max_pages=2048, layer_stride=1 << 40)
+    need = L.kda_attn_prefill_scratch_bytes(B, rows, total, ctypes.byref(kda.dims(heads, dim)), c)
+    assert need <= 2 * 148 * 256 * (dim + 4) * 4
+    busy = min(B, total)  # the same rows without the empty sequences
+    assert need <= L.kda_attn_prefill_scratch_bytes(busy, rows, total, ctypes.byref(kda.dims(heads, dim)), c)
