@@ -214,8 +214,14 @@ def _empty_on(nbytes: int, dev: int, stream_handle: int):
     import torch
     if torch.cuda.current_stream(dev).cuda_stream == stream_handle:
         return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream_handle, device=dev)):
+    with torch.cuda.stream(_stream_object(stream_handle, dev)):
         return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+
+
+def _stream_object(stream_handle: int, dev: int):
+    """torch's stream of a handle. 0 is the default stream; ExternalStream(0) would be a new stream of torch's own."""
+    import torch
+    return torch.cuda.ExternalStream(stream_handle, device=dev) if stream_handle else torch.cuda.default_stream(dev)
 
 
 def device_status(clear: bool = True) -> int:
@@ -721,7 +727,7 @@ def _attn_scratch(fn, key, d: KdaDims, cache: KVCache, stream, stream_handle: in
     if stream is None or _stream(None) == stream_handle:
         capturing = torch.cuda.is_current_stream_capturing()
     else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream_handle, device=cache._dev)):
+        with torch.cuda.stream(_stream_object(stream_handle, cache._device)):
             capturing = torch.cuda.is_current_stream_capturing()
     if capturing:
         return _empty_on(max(need, 16), cache._device, stream_handle)

@@ -236,3 +236,13 @@ def test_an_explicit_stream_and_its_capture():
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         check(*o, w)
+
+
+def test_scratch_of_the_default_stream_asked_for_on_another():
+    """stream=0 (the handle of the default stream) while another stream is current: the scratch is the default stream's memory."""
+    n, key = 48 << 20, (torch.cuda.current_device(), 0)
+    kda._SCRATCH.pop(key, None)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        at = kda.scratch_buffer(n, "cuda", 0).data_ptr()
+    kda._SCRATCH.pop(key)
+    assert torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr() == at  # given back to where it came from
