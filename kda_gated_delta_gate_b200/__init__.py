@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import threading
 from typing import Iterable, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -190,11 +191,21 @@ def t_pad(T: int, chunk: int = 64) -> int:
     return int(lib().kda_t_pad(T, chunk))
 
 
-# One scratch buffer per (device, stream), grown on demand and kept: the chunked prefill, varlen
-# and verify wrappers take it when the caller passes no `scratch`, so a hot call allocates only
+# One scratch buffer per (device, stream), grown on demand and kept: the chunked prefill, varlen,
+# verify and attention wrappers take it when the caller passes no `scratch`, so a hot call allocates only
 # the first time it needs more bytes on that stream. Calls on one stream are ordered, so they may
-# share its buffer; calls on different streams never do.
+# share its buffer; calls on different streams never do. A call is several launches, which host threads
+# with the same current stream could interleave: the ones that share a buffer are enqueued one call at a time.
 _SCRATCH = {}
+_ENQUEUE = threading.Lock()
+
+
+def _call_on(scratch, name: str, *args) -> int:
+    """_call; where the caller passed no scratch of its own, as one piece."""
+    if scratch is not None:
+        return _call(name, *args)
+    with _ENQUEUE:
+        return _call(name, *args)
 
 
 def scratch_buffer(nbytes: int, device, stream_handle: int):
@@ -253,9 +264,10 @@ def kda_chunk_prefill(q, k, v, gate, beta, h_state_ptrs, core, B: int, T: int, d
         return _call("kda_chunk_prefill_simt", _p(q), _p(k), _p(v), _p(gate), _p(beta), _p(h_state_ptrs), _p(core),
                      B, T, ctypes.byref(d), _stream(stream))
     st = _stream(stream)
+    own = scratch
     if scratch is None:
         scratch = scratch_buffer(kda_chunk_prefill_scratch_bytes(B, T, d), core.device, st)
-    return _call("kda_chunk_prefill", _p(q), _p(k), _p(v), _p(gate), _p(beta), _p(h_state_ptrs), _p(core), B, T,
+    return _call_on(own, "kda_chunk_prefill", _p(q), _p(k), _p(v), _p(gate), _p(beta), _p(h_state_ptrs), _p(core), B, T,
                  _p(scratch), scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
 
 
@@ -264,9 +276,10 @@ def kda_chunk_prefill_fused(qkv, g_raw, dt_bias, a_log, beta, h_state_ptrs, core
     """The chunked prefill on the front end's BF16 q|k|v rows and the raw BF16 gate input
     (the gate is formed in the kernel). `scratch` as for kda_chunk_prefill."""
     st = _stream(stream)
+    own = scratch
     if scratch is None:
         scratch = scratch_buffer(kda_chunk_prefill_scratch_bytes(B, T, d), core.device, st)
-    return _call("kda_chunk_prefill_fused", _p(qkv), _p(g_raw), _p(dt_bias), _p(a_log), _p(beta), _p(h_state_ptrs),
+    return _call_on(own, "kda_chunk_prefill_fused", _p(qkv), _p(g_raw), _p(dt_bias), _p(a_log), _p(beta), _p(h_state_ptrs),
                  _p(core), B, T, _p(scratch), scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
 
 
@@ -275,9 +288,10 @@ def kda_chunk_prefill_graw(q, k, v, g_raw, dt_bias, a_log, beta, h_state_ptrs, c
     """kda_chunk_prefill on FP32 q, k, v with the gate formed in the kernel from the raw BF16
     g_raw, dt_bias and a_log (bit-identical to kda_gate + kda_chunk_prefill)."""
     st = _stream(stream)
+    own = scratch
     if scratch is None:
         scratch = scratch_buffer(kda_chunk_prefill_scratch_bytes(B, T, d), core.device, st)
-    return _call("kda_chunk_prefill_graw", _p(q), _p(k), _p(v), _p(g_raw), _p(dt_bias), _p(a_log), _p(beta),
+    return _call_on(own, "kda_chunk_prefill_graw", _p(q), _p(k), _p(v), _p(g_raw), _p(dt_bias), _p(a_log), _p(beta),
                  _p(h_state_ptrs), _p(core), B, T, _p(scratch), scratch.numel() * scratch.element_size(),
                  ctypes.byref(d), st)
 
@@ -512,10 +526,11 @@ def kda_chunk_prefill_varlen(q, k, v, gate, beta, cu_seqlens, B: int, max_num_ch
                              h_state_ptrs, core, d: KdaDims, stream=None, scratch=None):
     """Chunked prefill over B packed sequences of unequal lengths (cu_seqlens: device int32 [B+1])."""
     st = _stream(stream)
+    own = scratch
     if scratch is None:
         need = int(lib().kda_chunk_prefill_varlen_scratch_bytes(B, max_num_chunks, ctypes.byref(d)))
         scratch = scratch_buffer(need, core.device, st)
-    return _call("kda_chunk_prefill_varlen", _p(q), _p(k), _p(v), _p(gate), _p(beta), _p(cu_seqlens), B,
+    return _call_on(own, "kda_chunk_prefill_varlen", _p(q), _p(k), _p(v), _p(gate), _p(beta), _p(cu_seqlens), B,
                  max_num_chunks, total_tokens, _p(h_state_ptrs), _p(core), _p(scratch),
                  scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
 
@@ -524,10 +539,11 @@ def kda_chunk_verify(q, k, v, gate, beta, cu_seqlens, B: int, total_tokens: int,
                      d: KdaDims, stream=None, scratch=None):
     """Batched verify: outputs for every draft row, states unchanged, tables kept for the fold."""
     st = _stream(stream)
+    own = scratch
     if scratch is None:
         need = int(lib().kda_chunk_prefill_varlen_scratch_bytes(B, 1, ctypes.byref(d)))
         scratch = scratch_buffer(need, core.device, st)
-    return _call("kda_chunk_verify", _p(q), _p(k), _p(v), _p(gate), _p(beta), _p(cu_seqlens), B, total_tokens,
+    return _call_on(own, "kda_chunk_verify", _p(q), _p(k), _p(v), _p(gate), _p(beta), _p(cu_seqlens), B, total_tokens,
                  _p(h_state_ptrs), _p(core), _p(tables), tables.numel() * tables.element_size(), _p(scratch),
                  scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
 
@@ -739,12 +755,13 @@ def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d
     """Attention of the last K tokens of each of N sequences over the cache (q, out [N*K, heads, head_dim] BF16,
     lse [N*K, heads] F32 or None). `scratch`: kda_attn_decode_scratch_bytes bytes; a cached buffer when None."""
     ref, st = _on(cache, stream)
+    own = scratch
     if scratch is None:
         scratch = _attn_scratch(kda_attn_decode_scratch_bytes, (N, K), d, cache, stream, st)
     elif scratch.device != cache._dev or not scratch.is_contiguous():
         raise ValueError(f"scratch is a contiguous tensor on {cache.k.device}")
     pq, po, pl = _attn_rows(cache, N * K, d, q, out, lse)
-    return _call("kda_attn_decode", ref, layer, pq, *_ints(cache, slots, n=N), N, K, window, sinks, po,
+    return _call_on(own, "kda_attn_decode", ref, layer, pq, *_ints(cache, slots, n=N), N, K, window, sinks, po,
                  pl, _p(scratch), scratch.numel() * scratch.element_size(), ctypes.byref(d), st)
 
 
@@ -754,11 +771,12 @@ def kda_attn_prefill(cache: KVCache, layer: int, q, cu_seqlens, slots, B: int, m
     [total_tokens, heads, head_dim] BF16, lse [total_tokens, heads] F32 or None). `scratch` as for
     kda_attn_decode (kda_attn_prefill_scratch_bytes)."""
     ref, st = _on(cache, stream)
+    own = scratch
     if scratch is None:
         scratch = _attn_scratch(kda_attn_prefill_scratch_bytes, (B, max_rows, total_tokens), d, cache, stream, st)
     elif scratch.device != cache._dev or not scratch.is_contiguous():
         raise ValueError(f"scratch is a contiguous tensor on {cache.k.device}")
     pq, po, pl = _attn_rows(cache, total_tokens, d, q, out, lse)
-    return _call("kda_attn_prefill", ref, layer, pq, *_ints(cache, cu_seqlens, n=B + 1), *_ints(cache, slots, n=B), B,
+    return _call_on(own, "kda_attn_prefill", ref, layer, pq, *_ints(cache, cu_seqlens, n=B + 1), *_ints(cache, slots, n=B), B,
                  max_rows, total_tokens, window, sinks, po, pl, _p(scratch), scratch.numel() * scratch.element_size(),
                  ctypes.byref(d), st)

@@ -246,3 +246,40 @@ def test_scratch_of_the_default_stream_asked_for_on_another():
         at = kda.scratch_buffer(n, "cuda", 0).data_ptr()
     kda._SCRATCH.pop(key)
     assert torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr() == at  # given back to where it came from
+
+
+def test_two_threads_on_one_stream():
+    """Decode, draft rows and packed rows from two host threads whose current stream is the same one."""
+    import threading
+    cs = [Case([1900, 31, 2500], [2] * 3, 8, 2, 128, 16, seed=s) for s in (21, 22)]
+    more = [Case([3000, 40], [90, 40], 4, 1, 64, 16, seed=s) for s in (23, 24)]
+    want, want_more = [run(c, 2) for c in cs], []
+
+    def packed(c):
+        out, lse = torch.empty_like(c.qd), torch.empty(c.qd.shape[:2], device="cuda")
+        kda.kda_attn_prefill(c.cache, 0, c.qd, cu, None, 2, 90, c.total, out, c.d, lse=lse)
+        return out, lse
+
+    cu = i32(more[0].cu)
+    want_more = [packed(c) for c in more]
+    stream, got = torch.cuda.current_stream(), [[], []]
+
+    def work(i):
+        with torch.cuda.stream(stream):
+            for _ in range(40):
+                got[i].append((run(cs[i], 2), packed(more[i])))
+
+    torch.cuda.synchronize()
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        check(*want[i], cs[i].expected())
+        check(*want_more[i], more[i].expected())
+        assert len(got[i]) == 40
+        for a, b in got[i]:
+            assert torch.equal(a[0], want[i][0]) and torch.equal(a[1], want[i][1])
+            assert torch.equal(b[0], want_more[i][0]) and torch.equal(b[1], want_more[i][1])

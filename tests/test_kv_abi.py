@@ -199,3 +199,46 @@ def test_scratch_does_not_grow_with_sequences_without_rows(L, B, rows, total, he
     assert need <= 2 * 148 * 256 * (dim + 4) * 4
     busy = min(B, total)  # the same rows without the empty sequences
     assert need <= L.kda_attn_prefill_scratch_bytes(busy, rows, total, ctypes.byref(kda.dims(heads, dim)), c)
+
+
+def test_calls_of_two_threads_that_share_scratch_do_not_mix(L, monkeypatch):
+    """A call that takes the stream's cached scratch launches several kernels on it: another thread's call on the stream comes
+    before or after all of them. With scratch of their own, calls of two threads may run side by side."""
+    import threading
+    import time
+    bf = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32)
+    scr, d = torch.zeros(64, dtype=torch.uint8), kda.dims(4, 64)
+    c = kda.KVCache(bf(1, 4, 2, 16, 64), bf(1, 4, 2, 16, 64), torch.zeros(3, 5, dtype=torch.int32), ints(0, 0, 0), ints(0, 0, 0, 0))
+    inside, most = [0], [0]
+
+    def slow_call(name, *args):
+        inside[0] += 1
+        most[0] = max(most[0], inside[0])
+        time.sleep(0.02)
+        inside[0] -= 1
+
+    monkeypatch.setattr(kda, "_on", lambda cache, stream: (cache._ref, 5))
+    monkeypatch.setattr(kda, "_call", slow_call)
+    monkeypatch.setattr(kda, "_attn_scratch", lambda *a: scr)
+    monkeypatch.setattr(kda, "scratch_buffer", lambda *a: scr)
+    q, x = bf(4, 4, 64), torch.zeros(64, 4, 64)
+    calls = [lambda **k: kda.kda_attn_decode(c, 0, q, None, 4, 1, q, d, **k),
+             lambda **k: kda.kda_attn_prefill(c, 0, q, ints(0, 1, 4), None, 2, 4, 4, q, d, **k),
+             lambda **k: kda.kda_chunk_prefill(x, x, x, x, x, x, x, 1, 64, d, stream=5, **k),
+             lambda **k: kda.kda_chunk_prefill_fused(x, x, x, x, x, x, x, 1, 64, d, stream=5, **k),
+             lambda **k: kda.kda_chunk_prefill_graw(x, x, x, x, x, x, x, x, x, 1, 64, d, stream=5, **k),
+             lambda **k: kda.kda_chunk_prefill_varlen(x, x, x, x, x, x, 1, 1, 64, x, x, d, stream=5, **k),
+             lambda **k: kda.kda_chunk_verify(x, x, x, x, x, x, 1, 64, x, x, x, d, stream=5, **k)]
+
+    def together(**k):
+        inside[0] = most[0] = 0
+        ts = [threading.Thread(target=f, kwargs=k) for f in calls for _ in range(2)]
+        for t in ts:
+            t.start()
+        for t in ts:
+            t.join()
+        return most[0]
+
+    assert together() == 1
+    assert together(scratch=scr) > 1
