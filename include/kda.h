@@ -87,6 +87,11 @@ KDA_API size_t kda_t_pad(size_t T, int chunk);
  * Synchronises the device. Returns KDA_OK or KDA_ERR_CUDA. */
 KDA_API int kda_device_status(int *out, int clear);
 
+/* The number of the capture that `stream` is in (HOST *id; unique in the process, never 0), or 0 if the
+ * stream is not being captured. KDA_ERR_INVALID_ARG (id NULL). A stream that cannot be asked (the default stream while
+ * another stream is being captured) is in none. Launches nothing. */
+KDA_API int kda_stream_capture_id(void *stream, unsigned long long *id);
+
 /* ---------------------------------------------------------------------------------
  * kda_gate — the bounded log-decay gate (Glm5NextKdaWorkspace, field `gate`, from
  * field `g_raw`; Glm5NextKdaWeights, `dt_bias` per channel, `a_log` per head):

@@ -67,6 +67,7 @@ _SIGS = {
     "kda_version": ([], _I),
     "kda_status_string": ([_I], ctypes.c_char_p),
     "kda_t_pad": ([ctypes.c_size_t, _I], ctypes.c_size_t),
+    "kda_stream_capture_id": ([_VP, ctypes.POINTER(ctypes.c_ulonglong)], _I),
     "kda_device_status": ([ctypes.POINTER(_I), _I], _I),
     "kda_gate": ([_VP, _VP, _VP, _VP, _I, _DIMS, _VP], _I),
     "kda_beta": ([_VP, _VP, _I, _VP], _I),
@@ -733,7 +734,7 @@ def kda_attn_prefill_scratch_bytes(B: int, max_rows: int, total_tokens: int, d: 
 
 def _attn_scratch(fn, key, d: KdaDims, cache: KVCache, stream, stream_handle: int):
     """The stream's cached buffer, of at least fn(*key) bytes; while the stream is being captured a buffer of the
-    graph's own, so that graphs captured one after the other may run at once."""
+    graph's own (_graph_scratch), so that graphs captured one after the other may run at once."""
     torch = cache._torch
     need = cache._need.get((key, d.heads, d.head_dim))
     if need is None:
@@ -743,11 +744,53 @@ def _attn_scratch(fn, key, d: KdaDims, cache: KVCache, stream, stream_handle: in
     if stream is None or _stream(None) == stream_handle:
         capturing = torch.cuda.is_current_stream_capturing()
     else:
-        with torch.cuda.stream(_stream_object(stream_handle, cache._device)):
-            capturing = torch.cuda.is_current_stream_capturing()
+        capturing = _capture_id(stream_handle) != 0
     if capturing:
-        return _empty_on(max(need, 16), cache._device, stream_handle)
+        return _graph_scratch(max(need, 16), cache._device, stream_handle)
     return scratch_buffer(need, cache._dev, stream_handle)
+
+
+_GRAPHS = {}  # (device, stream, capture) -> None: the allocator has a pool for the graph; else the buffer kept for it
+_KEPT = []    # every such buffer
+
+
+def _graph_scratch(nbytes: int, dev: int, stream_handle: int):
+    """Scratch for the graph that the stream is being captured into. Under torch.cuda.graph it is memory of the graph's own
+    allocator pool, which stays with the graph. Where the stream is captured in another way (the CUDA API itself) it would go
+    back to the ordinary pool when the call returns, and later tensors would share it with the graph's replays: there one
+    buffer per capture is kept for good; callers that capture many such graphs pass `scratch`."""
+    key = (dev, stream_handle, _capture_id(stream_handle))
+    kept = _GRAPHS.get(key)
+    if kept is not None and kept.numel() >= nbytes:
+        return kept
+    buf = _empty_on(nbytes, dev, stream_handle)
+    if kept is not None or (key not in _GRAPHS and not _of_a_pool(buf)):
+        _GRAPHS[key] = buf
+        _KEPT.append(buf)
+    elif key not in _GRAPHS:
+        if len(_GRAPHS) >= 1024:
+            _GRAPHS.clear()
+        _GRAPHS[key] = None
+    return buf
+
+
+def _of_a_pool(t) -> bool:
+    """Whether tensor t lies in one of the allocator's pools for graphs (about 1 us a segment: asked once per capture)."""
+    import torch
+    try:
+        segments = torch.cuda.memory_snapshot()
+    except RuntimeError:  # another allocator, whose memory the graph holds itself
+        return True
+    at, dev = t.data_ptr(), t.device.index
+    return any(tuple(g["segment_pool_id"]) != (0, 0) for g in segments
+               if g["device"] == dev and g["address"] <= at < g["address"] + g["total_size"])
+
+
+def _capture_id(stream_handle: int) -> int:
+    """The number of the capture that the stream is in, 0 if it is in none."""
+    out = ctypes.c_ulonglong(0)
+    _call("kda_stream_capture_id", stream_handle, ctypes.byref(out))
+    return out.value
 
 
 def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d: KdaDims, window: int = 0,

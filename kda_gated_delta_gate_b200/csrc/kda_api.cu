@@ -74,6 +74,18 @@ const char *kda_status_string(int status) {
     }
 }
 
+int kda_stream_capture_id(void *stream, unsigned long long *id) {
+    if (!id) return KDA_ERR_INVALID_ARG;
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    unsigned long long n = 0;
+    if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &st, &n) != cudaSuccess) {
+        cudaGetLastError();
+        st = cudaStreamCaptureStatusNone;
+    }
+    *id = st == cudaStreamCaptureStatusActive ? n + 1 : 0;
+    return KDA_OK;
+}
+
 size_t kda_t_pad(size_t T, int chunk) {
     if (chunk <= 0) return 0;
     const size_t c = static_cast<size_t>(chunk);

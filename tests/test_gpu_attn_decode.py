@@ -283,3 +283,55 @@ def test_two_threads_on_one_stream():
         for a, b in got[i]:
             assert torch.equal(a[0], want[i][0]) and torch.equal(a[1], want[i][1])
             assert torch.equal(b[0], want_more[i][0]) and torch.equal(b[1], want_more[i][1])
+
+
+def test_a_stream_captured_through_the_cuda_api(monkeypatch):
+    """Captured by cudaStreamBeginCapture, no allocator pool stands behind the graph: its scratch stays its own."""
+    import ctypes
+    rt = ctypes.CDLL("libcudart.so.12")
+    ok = lambda rc: rc == 0 or pytest.fail(f"cuda error {rc}")
+    c = Case([900, 31, 2000], [1] * 3, 8, 2, 128, 16, seed=31)
+    want, slots = c.expected(), i32(c.order)
+    out, lse = torch.zeros_like(c.qd), torch.zeros((3, 8), device="cuda")
+    made, empty_on = [], kda._empty_on
+
+    def noted(*a):
+        buf = empty_on(*a)
+        made.append((buf.data_ptr(), buf.numel()))
+        return buf
+
+    monkeypatch.setattr(kda, "_empty_on", noted)
+    side = torch.cuda.Stream()
+    call = lambda: kda.kda_attn_decode(c.cache, 0, c.qd, slots, 3, 1, out, c.d, lse=lse, stream=side)
+    call()
+    torch.cuda.synchronize()
+    made.clear()
+    st, graph, ex = ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p(), ctypes.c_void_p()
+    ok(rt.cudaStreamBeginCapture(st, 1))  # thread-local mode
+    call()
+    call()
+    ok(rt.cudaStreamEndCapture(st, ctypes.byref(graph)))
+    assert len(made) == 1  # both calls are on one stream
+    ok(rt.cudaGraphInstantiate(ctypes.byref(ex), graph, ctypes.c_ulonglong(0)))
+    at, n = made[0]
+    with torch.cuda.stream(side):
+        later = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for t in later:
+        assert t.data_ptr() + n <= at or at + n <= t.data_ptr()
+    out.zero_(), lse.zero_()
+    torch.cuda.synchronize()
+    ok(rt.cudaGraphLaunch(ex, st))
+    torch.cuda.synchronize()
+    check(out, lse, want)
+    for t in later:
+        assert (t == 255).all()
+    ok(rt.cudaGraphExecDestroy(ex))
+    ok(rt.cudaGraphDestroy(graph))
+    # torch's own capture: the graph's pool has the memory, nothing is kept
+    before, g = len(kda._KEPT), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kda.kda_attn_decode(c.cache, 0, c.qd, slots, 3, 1, out, c.d, lse=lse)
+    out.zero_()
+    g.replay()
+    check(out, lse, want)
+    assert len(kda._KEPT) == before

@@ -242,3 +242,26 @@ def test_calls_of_two_threads_that_share_scratch_do_not_mix(L, monkeypatch):
 
     assert together() == 1
     assert together(scratch=scr) > 1
+
+
+def test_capture_id_arguments(L):
+    assert L.kda_stream_capture_id(None, None) == 1
+    n = ctypes.c_ulonglong(7)
+    assert L.kda_stream_capture_id(None, ctypes.byref(n)) == 0 and n.value == 0
+
+
+def test_scratch_of_a_graph_is_kept_where_the_allocator_has_no_pool_for_it(monkeypatch):
+    made, pooled, capture = [], [True], [1]
+    monkeypatch.setattr(kda, "_empty_on", lambda n, dev, st: made.append(torch.zeros(n, dtype=torch.uint8)) or made[-1])
+    monkeypatch.setattr(kda, "_of_a_pool", lambda t: pooled[0])
+    monkeypatch.setattr(kda, "_capture_id", lambda st: capture[0])
+    monkeypatch.setattr(kda, "_GRAPHS", {})
+    monkeypatch.setattr(kda, "_KEPT", [])
+    assert kda._graph_scratch(64, 0, 5) is made[0] and kda._graph_scratch(64, 0, 5) is made[1] and not kda._KEPT
+    pooled[0], capture[0] = False, 2
+    a = kda._graph_scratch(64, 0, 5)
+    assert kda._graph_scratch(32, 0, 5) is a and kda._graph_scratch(64, 0, 6) is not a  # another stream of the capture
+    b = kda._graph_scratch(96, 0, 5)
+    assert b is not a and kda._graph_scratch(96, 0, 5) is b and any(x is a for x in kda._KEPT) and any(x is b for x in kda._KEPT)
+    capture[0] = 3
+    assert kda._graph_scratch(64, 0, 5) is not b and len(kda._KEPT) == 4
