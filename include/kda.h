@@ -708,9 +708,10 @@ KDA_API int kda_kv_compact(const kda_kv_cache *cache, int *live, void *stream);
  *   k_new, v_new  [total_tokens, kv_heads * head_dim] BF16, row stride ld elements (a multiple of 8, so
  *                 the k and v columns of packed q|k|v projection rows can be passed as they are)
  *   cu_seqlens    DEVICE int32 [B + 1];  slots  DEVICE int32 [B] or NULL (slot i)
- * Rows at or past cu_seqlens[B] are not read. A sequence with bad bounds, a slot out of range or listed
- * before, more rows than tokens, or a row whose table entry is no page or a page that several slots
- * share is skipped and latches KDA_ERR_INVALID_ARG. */
+ * Rows at or past cu_seqlens[B] are not read. A sequence with bad bounds (negative, decreasing, past total_tokens or
+ * past cu_seqlens[B]; where cu_seqlens decreases, rows of its other sequences too), a slot out of range or listed
+ * before, or more rows than tokens is skipped, and so is a row whose table entry is no page or a page that several
+ * slots share; each latches KDA_ERR_INVALID_ARG. kv_heads * head_dim <= 2^20 (else KDA_ERR_UNSUPPORTED). */
 KDA_API int kda_kv_append(const kda_kv_cache *cache, int layer, const kda_bf16 *k_new, const kda_bf16 *v_new,
                           long long ld, const int *cu_seqlens, const int *slots, int B, int total_tokens,
                           void *stream);

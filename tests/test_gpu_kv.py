@@ -190,3 +190,49 @@ def test_large_pools_and_many_slots():
     got = c.page_table[0, 39]
     assert torch.equal(c.k[0, got, :, 3].reshape(-1), probe[0]) and torch.equal(c.v[0, got, :, 3].reshape(-1), -probe[0])
     assert int(c.page_table.max()) == int(live) - 1 and len(keep) == 100
+
+
+def _append_with_bounds(p, cu, slots, total):
+    """kda_kv_append with any bounds, against the rows that its description lets through: of a sequence whose bounds are
+    0 <= cu[b] <= cu[b + 1] <= min(total, cu[B]); where cu decreases these may stay as they were too."""
+    c, m = p.cache, p.model
+    before = m.k.copy(), m.v.copy()
+    w = c.k.shape[2] * c.k.shape[4]
+    k_new, v_new = (torch.from_numpy(p.rng.standard_normal((total, w), dtype=np.float32)).cuda().bfloat16() for _ in range(2))
+    kda.kda_kv_append(c, 0, k_new, v_new, _i32(cu), _i32(slots), len(slots), total)
+    kb, vb = (_bits(t).reshape(-1, c.k.shape[2], c.k.shape[4]) for t in (k_new, v_new))
+    for b, s in enumerate(slots):
+        if 0 <= cu[b] <= cu[b + 1] <= min(total, cu[-1]):
+            m.append(0, kb[cu[b]:cu[b + 1]], vb[cu[b]:cu[b + 1]], [0, cu[b + 1] - cu[b]], [s])
+        else:
+            m.status = 1
+    if any(b < a for a, b in zip(cu, cu[1:])):
+        assert m.status == 1
+        m.k, m.v = (np.where((new == got).all(-1, keepdims=True), new, old) for new, old, got in
+                    ((m.k, before[0], _bits(c.k)), (m.v, before[1], _bits(c.v))))
+    p.check()
+
+
+@pytest.mark.parametrize("cu", [[0, 4, 2, 6], [0, -4, 2, 6], [0, 2, 99, 6], [-1, 2, 4, 6], [2 ** 31 - 1, -2 ** 31, 3, 6], [0, 2, 4, 99],
+                                [0, 2, 4, -1], [6, 4, 2, 0], [0, 0, 6, 3], [3, 5, 4, 6]])
+def test_append_bad_bounds_of_sequences_with_room(cu):
+    """Slots that hold enough tokens in pages of their own, so that only the bounds can refuse a row."""
+    p = Pair(pages=12, page=16, seqs=3, max_pages=4)
+    p.call("reserve", [0, 1, 2], [32, 32, 32])
+    _append_with_bounds(p, cu, [2, 0, 1], 6)
+
+
+@pytest.mark.parametrize("wrong", [{700: -5}, {700: 2 ** 31 - 1}, {3: 900, 1400: 2}, {0: -1}, {i: -i for i in range(1, 1500, 2)}, {1500: 40}])
+def test_append_bad_bounds_among_many_sequences(wrong):
+    """More sequences than the rows' blocks mark one by one."""
+    n = 1500
+    p = Pair(pages=n + 20, page=16, heads=1, seqs=n, max_pages=1, layers=1)
+    kda.kda_kv_reserve(p.cache, None, _i32([3] * n), n)
+    p.model.reserve(range(n), [3] * n)
+    rows = [(i * 7) % 3 for i in range(n)]
+    cu = [0] + np.cumsum(rows).tolist()
+    total = cu[-1]
+    for i, x in wrong.items():
+        cu[i] = x
+    order = [int(x) for x in np.random.default_rng(5).permutation(n)]
+    _append_with_bounds(p, cu, order, total)
