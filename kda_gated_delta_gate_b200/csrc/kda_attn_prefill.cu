@@ -321,10 +321,9 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
 
     // TMEM and barriers by two of the warps that do not compute, under every warp's search for the tile
     if (warp == W + 3) {  // CTA b looks sequence b over, and where there are fewer CTAs its other lanes those further on
-        for (long long b = blockIdx.x + static_cast<long long>(lane) * gridDim.x; b < a.B; b += 32LL * gridDim.x) {
-            int c0, c1, s, len;
-            if (!sequence(a, static_cast<int>(b), c0, c1, s, len)) atomicExch(a.status, KDA_ERR_INVALID_ARG);
-        }
+        const long long b = blockIdx.x + static_cast<long long>(lane) * gridDim.x;  // the grid is at least B / 32
+        int c0, c1, s, len;
+        if (b < a.B && !sequence(a, static_cast<int>(b), c0, c1, s, len)) atomicExch(a.status, KDA_ERR_INVALID_ARG);
     }
     if (warp == W + 2 && lane == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -786,7 +785,9 @@ template <int D>
 int launch_prefill(const PrefillArgs &a, unsigned grid, cudaStream_t s) {
     static std::atomic<unsigned long long> attr{0};
     KDA_TRY(smem_opt_in(prefill_kernel<D>, PrefillCfg<D>::BYTES, attr));
-    prefill_kernel<D><<<grid * a.splits, PrefillCfg<D>::THREADS, PrefillCfg<D>::BYTES, s>>>(a);
+    // CTAs beyond the tiles' only look sequences over, 32 each (a loop there made the softmax warps spill)
+    const unsigned ctas = std::max(grid * a.splits, static_cast<unsigned>((a.B + 31LL) / 32));
+    prefill_kernel<D><<<ctas, PrefillCfg<D>::THREADS, PrefillCfg<D>::BYTES, s>>>(a);
     KDA_TRY(launch_status());
     if (a.splits == 1) return KDA_OK;
     return launch_after(prefill_join_kernel<D>, dim3(grid, tile_rows(D) / 8), dim3(256), 0, s, a);

@@ -290,7 +290,8 @@ def test_serving_run():
 
 @pytest.mark.parametrize("B,busy,heads,kv_heads,dim", [(2000, {3: (2100, 3), 1998: (700, 2)}, 32, 2, 128),
                                                        (300, {0: (900, 140), 150: (40, 1), 299: (1300, 60)}, 4, 1, 64),
-                                                       (70, {64: (600, 1)}, 33, 1, 64)])
+                                                       (70, {64: (600, 1)}, 33, 1, 64),
+                                                       (6000, {4000: (300, 1)}, 33, 1, 128)])
 def test_few_sequences_with_rows_among_many_without(B, busy, heads, kv_heads, dim):
     """A fixed list of slots, most of them without rows: fewer row tiles than sequences, walks shared by several CTAs."""
     lens, rows = [i % 3 for i in range(B)], [0] * B
@@ -303,3 +304,25 @@ def test_few_sequences_with_rows_among_many_without(B, busy, heads, kv_heads, di
     again = run(c)
     assert kda.device_status(clear=True) == 1
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("lens,rows,heads,kv_heads,dim,window", [([2500], [2500], 8, 2, 128, 0), ([2500], [2500], 8, 2, 64, 0),
+                                                                 ([900, 640], [300, 640], 8, 4, 64, 200), ([6000], [140], 4, 1, 128, 0),
+                                                                 ([5000], [300], 2, 1, 64, 0), ([900, 31, 2000], [4, 4, 4], 8, 2, 128, 0),
+                                                                 ([900, 31, 2000], [1, 1, 1], 8, 2, 64, 0), ([700, 90], [16, 16], 8, 2, 128, 0)])
+def test_equal_values_come_out_as_they_are(lens, rows, heads, kv_heads, dim, window):
+    """V rows that are all c: the weights, whatever they are rounded to, are divided by their own sum, and o is c. Weights and
+    products are summed in FP32, each sum within 6000 2^-24 < 2^-11 of the terms, so o is within 2^-10 of c before its own
+    rounding, and what is nearer than 2^-9 to a BF16 value rounds to it."""
+    c = Case(lens, rows, heads, kv_heads, dim, 16, window, seed=dim + heads, spread=4.0)
+    value = torch.randn((kv_heads, dim), generator=torch.Generator().manual_seed(7)).bfloat16().cuda()
+    c.cache.v.copy_(value[:, None].expand(kv_heads, 16, dim).expand_as(c.cache.v))
+    out, lse = run(c)
+    want = value.repeat_interleave(heads // kv_heads, 0).expand_as(out)
+    assert torch.equal(out, want), f"{int((out != want).sum())} of {out.numel()} values differ"
+    if len(set(rows)) == 1:
+        n = rows[0]
+        if heads // kv_heads * n <= 64:
+            o = torch.empty_like(out)
+            kda.kda_attn_decode(c.cache, 0, c.qd, None, len(lens), n, o, c.d, window=window)
+            assert torch.equal(o, want)
