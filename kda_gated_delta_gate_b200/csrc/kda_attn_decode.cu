@@ -15,7 +15,7 @@
 // With at most 16 query rows each warp takes a quarter of the tile's keys and its own m, l and o, joined at the pair's
 // end; with up to 32 two warps share a key half. With at most 8 the products are turned round (RowsShort). mma.sync is
 // enough: at 16 rows the products need about a sixth of its rate while HBM is saturated.
-// p is rounded to BF16 for the second product (at most 2^-9 of each weight); the sum that o is divided by is that of the
+// p is rounded to BF16 for the second product (at most 2^-8 of each weight); the sum that o is divided by is that of the
 // rounded p (one more product, with ones), so that the roundings cancel where few keys carry a row, and the one that
 // lse takes is that of the unrounded p.
 //

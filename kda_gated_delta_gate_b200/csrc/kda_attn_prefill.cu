@@ -18,8 +18,11 @@
 //               next S is formed as soon as this one is in registers.
 //   zeros       in the V rows of edge tiles that no row of the CTA sees
 // O is rescaled only when a row's maximum has grown by more than 2^8 since its reference was set (P then
-// stays below 2^8, harmless in BF16 and FP32). P is rounded to BF16 for the second product (at most 2^-9 of each weight);
-// l sums the unrounded P.
+// stays below 2^8, harmless in BF16 and FP32). P is rounded to BF16 for the second product (at most 2^-8 of each weight).
+// O is divided by the sum of the rounded weights, as in the one-token form, so that a row that few keys carry is not scaled by
+// their roundings (V rows that are all alike come out as they are); lse takes the sum of the unrounded ones. The second
+// sum costs two additions per pair of weights: 452 us against 442 for 8192 tokens at head_dim 128, 421 against 390 at 64 (these
+// are additions of BF16 to FP32; by shifts and masks 472 and 447, as products with ones by mma.sync 636 and 482).
 // Where the tiles are fewer than the SMs, several CTAs share a walk and prefill_join_kernel adds their parts in order.
 //
 // Rows of a cache tile that no row of the CTA sees (past the last token, before the window, pages that
@@ -68,7 +71,7 @@ struct PrefillArgs {
     int B, max_rows, total, heads, G, window, sinks, nslots;
     int splits;             // CTAs that share a tile's walk; above 1 each leaves a part
     float *part_o;          // [slot][kv head][split][256][D]
-    float *part_ml;         // [slot][kv head][split][256][2]
+    float *part_ml;         // [slot][kv head][split][256][4]: m, l (-1: bad page), l of the rounded P
     float scale2;  // |scale| log2(e)
     uint32_t flip;  // sign bits of a BF16 pair if scale < 0 (the queries are negated), else 0
 };
@@ -193,6 +196,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// lo and hi plus the two BF16 values of u.
+__device__ __forceinline__ void add_halves(float &lo, float &hi, uint32_t u) {
+    asm("{\n\t.reg .b16 x, y;\n\t"
+        "mov.b32 {x, y}, %2;\n\t"
+        "add.rn.f32.bf16 %0, x, %0;\n\t"
+        "add.rn.f32.bf16 %1, y, %1;\n\t}\n"
+        : "+f"(lo), "+f"(hi)
+        : "r"(u));
 }
 
 // True in one lane of a converged warp. The MMA role runs with its whole warp and branches on this around the
@@ -558,7 +571,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
         const uint32_t ts = tmem_lane_base(tmem, warp) + 128 * x, to = tmem_lane_base(tmem, warp) + C::COL_O + D * x;
         const uint32_t tp = tmem_lane_base(tmem, warp) + C::COL_P + C::STEP_P * x;
         const int p_first = t.base + (t.r0 + 128 * x) / a.G, p_last = x ? t.p_hi_b : t.p_hi_a, tiles = x ? t.tiles_b : t.tiles_a;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, lr = 0.f;  // lr: the sum of the rounded weights
         bool ok = true;
         for (int i = 0; i < tiles; ++i) {
             if (!(ok = wait_or_abort(&sfull[x], i & 1, abort, a.status))) break;
@@ -615,9 +628,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
                 }
             }
             l *= f;
+            lr *= f;
             const float ref = m == -INFINITY ? 0.f : m;
             const uint64_t scale_2 = pair(a.scale2, a.scale2), ref_2 = pair(-ref, -ref);
             uint64_t sum[2] = {0ull, 0ull};
+            float rsum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < kKeys; c += 32) {
                 uint32_t u[16];
@@ -631,6 +646,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
                     u[e] = pack_bf16(p0, p1);
                 }
                 tmem_st16(tp + c / 2, u);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) add_halves(rsum[e & 1], rsum[2 + (e & 1)], u[e]);
                 if (c == 32 || c == 96) {  // 64 keys' weights are there: their half of the product may start
                     tmem_st_wait();
                     tc_fence_before();
@@ -641,12 +658,13 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
             float sum_lo, sum_hi;
             unpair(add2(sum[0], sum[1]), sum_lo, sum_hi);
             l += sum_lo + sum_hi;
+            lr += (rsum[0] + rsum[1]) + (rsum[2] + rsum[3]);
         }
         // a half that sees nothing waits for the other, so that both know of a bad page
         if (ok && tiles > 0) ok = wait_or_abort(&ofull[x], C::OWN_P ? (tiles - 1) & 1 : 0, abort, a.status);
         else if (ok && ntiles > 0) ok = wait_or_abort(&ofull[x ^ 1], 0, abort, a.status);
         tc_fence_after();
-        if (splits > 1) {  // this part's l, m and unscaled O; l = -1: a page was none
+        if (splits > 1) {  // this part's sums, m and unscaled O; l = -1: a page was none
             const size_t pr = (static_cast<size_t>(slot_id) * hk + h) * a.splits * C::ROWS + static_cast<size_t>(split) * C::ROWS + r;
             float4 *const dst = reinterpret_cast<float4 *>(a.part_o + pr * D);
 #pragma unroll 1
@@ -659,10 +677,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::THREADS, PrefillCfg<D>::CTAS) p
                     for (int e = 0; e < 16; e += 4) dst[(c + e) / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
-            *reinterpret_cast<float2 *>(a.part_ml + 2 * pr) = make_float2(m, ok && !*bad_page ? l : -1.f);
+            *reinterpret_cast<float4 *>(a.part_ml + 4 * pr) = make_float4(m, ok && !*bad_page ? l : -1.f, lr, 0.f);
             if (*bad_page && tid == 0) atomicExch(a.status, KDA_ERR_INVALID_ARG);
         } else if (__all_sync(0xffffffffu, ok && !*bad_page)) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float inv = l == 0.f ? 0.f : 1.f / lr;
             uint8_t *const rows_sm = sm + x * C::TILE + 32 * (warp & 3) * 128;  // Q has been read
             int ln = lane;  // hidden from the compiler, which would keep the addresses of Q's copy in registers for this one
             asm volatile("" : "+r"(ln));
@@ -718,36 +736,37 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
     if (!locate<R>(a, slot, t)) return;
     const int splits = parts_of(a, t);
     if (splits == 1) return;
-    const float *const ml = a.part_ml + 2 * (static_cast<size_t>(slot) * hk + h) * a.splits * R;
+    const float4 *const ml = reinterpret_cast<const float4 *>(a.part_ml) + (static_cast<size_t>(slot) * hk + h) * a.splits * R;
     const float *const po = a.part_o + (static_cast<size_t>(slot) * hk + h) * a.splits * R * D;
     const int r = 8 * blockIdx.y + (threadIdx.x >> 5);
     if (r >= t.rows) return;
     float m = -INFINITY;
     bool bad = false;
     for (int p = 0; p < splits; ++p) {
-        m = fmaxf(m, ml[2 * (p * R + r)]);
-        bad |= ml[2 * (p * R + r) + 1] == -1.f;
+        m = fmaxf(m, ml[p * R + r].x);
+        bad |= ml[p * R + r].y == -1.f;
     }
     // a page that is none leaves the whole tile, as an unsplit walk does
     for (int p = 0; p < splits; ++p)
-        for (int k = lane; k < t.rows; k += 32) bad |= ml[2 * (p * R + k) + 1] == -1.f;
+        for (int k = lane; k < t.rows; k += 32) bad |= ml[p * R + k].y == -1.f;
     if (__any_sync(0xffffffffu, bad)) return;
-    float l = 0.f, o[E];
+    float l = 0.f, lr = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
     for (int p = 0; p < splits; ++p) {
-        const float lp = ml[2 * (p * R + r) + 1];
-        if (lp == 0.f) continue;  // that part saw nothing and left no O
-        const float w = ex2(ml[2 * (p * R + r)] - m);
-        l = fmaf(lp, w, l);
+        const float4 part = ml[p * R + r];
+        if (part.y == 0.f) continue;  // that part saw nothing and left no O
+        const float w = ex2(part.x - m);
+        l = fmaf(part.y, w, l);
+        lr = fmaf(part.z, w, lr);
         const float *const src = po + (static_cast<size_t>(p) * R + r) * D + E * lane;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], w, o[e]);
     }
     const int q = t.r0 + r, tok = q / a.G;
     const size_t row = static_cast<size_t>(t.c0 + tok) * a.heads + static_cast<size_t>(h) * a.G + (q - tok * a.G);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : 1.f / lr;
     uint32_t u[E / 2];
 #pragma unroll
     for (int e = 0; e < E; e += 2) u[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
