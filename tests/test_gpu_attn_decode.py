@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import kda_gated_delta_gate_b200 as kda
+import oracle
 from tests.attn_harness import Case, check, i32
 
 pytestmark = pytest.mark.gpu
@@ -335,3 +336,32 @@ def test_a_stream_captured_through_the_cuda_api(monkeypatch):
     g.replay()
     check(out, lse, want)
     assert len(kda._KEPT) == before
+
+
+def test_more_sequences_than_a_grid_dimension_has():
+    """70000 sequences, a few of them long, one of them refused."""
+    n, page = 70000, 16
+    lens = [1 + i % 3 for i in range(n)]
+    for i, x in ((17, 160), (40000, 90), (69999, 33)):
+        lens[i] = x
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()
+    pages, heads = n + 20, 2
+    cache = kda.KVCache.empty(pages, page, 1, 64, n, 10)
+    cache.k.copy_(rand(*cache.k.shape))
+    cache.v.copy_(rand(*cache.v.shape))
+    kda.kda_kv_reserve(cache, None, i32(lens), n)
+    q = rand(n, heads, 64)
+    d, out, lse = kda.dims(heads, 64, scale=0.125), torch.full_like(q, float("nan")), torch.empty((n, heads), device="cuda")
+    cache.seq_len[123] = -1
+    kda.kda_attn_decode(cache, 0, q, None, n, 1, out, d, lse=lse)
+    assert kda.device_status(clear=True) == 1 and torch.isnan(out[123]).all()
+    out[123] = 0
+    assert torch.isfinite(out).all()
+    table = cache.page_table.cpu()
+    for i in (0, 1, 17, 122, 124, 33333, 40000, 69998, 69999):
+        rows = [cache.k[0, table[i, j], 0].cpu().double() for j in range(-(-lens[i] // page))]
+        vals = [cache.v[0, table[i, j], 0].cpu().double() for j in range(-(-lens[i] // page))]
+        k, v = torch.cat(rows)[:lens[i]].numpy(), torch.cat(vals)[:lens[i]].numpy()
+        o, l, sp = zip(*[oracle.attention(q[i, h:h + 1].double().cpu().numpy(), k, v, [lens[i] - 1], 0.125) for h in range(heads)])
+        check(out[i:i + 1], lse[i:i + 1], (np.stack(o, 1), np.stack(l, 1), np.stack(sp, 1)))

@@ -326,3 +326,37 @@ def test_equal_values_come_out_as_they_are(lens, rows, heads, kv_heads, dim, win
             o = torch.empty_like(out)
             kda.kda_attn_decode(c.cache, 0, c.qd, None, len(lens), n, o, c.d, window=window)
             assert torch.equal(o, want)
+
+
+def test_both_head_sizes_and_the_short_form_at_once():
+    """Packed calls at head_dim 64 and 128 (256 and 512 TMEM columns per CTA) and decodes, on three streams."""
+    cs = [Case([700, 31, 900], [500, 31, 200], 8, 2, dim, 32, seed=dim) for dim in (64, 128)]
+    one = Case([900, 31, 2000], [1] * 3, 8, 2, 128, 16, seed=41)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs, o1, l1 = [None, None], torch.empty_like(one.qd), torch.empty((3, 8), device="cuda")
+    slots = i32(one.order)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, c in enumerate(cs):
+            with torch.cuda.stream(streams[i]):
+                outs[i] = run(c)
+        kda.kda_attn_decode(one.cache, 0, one.qd, slots, 3, 1, o1, one.d, lse=l1, stream=streams[2])
+    torch.cuda.synchronize()
+    for c, o in zip(cs, outs):
+        check(*o, c.expected())
+    check(o1, l1, one.expected())
+
+
+def test_more_heads_per_kv_head_than_a_tile_has_rows():
+    c = Case([150, 3, 40], [3, 1, 0], 600, 2, 64, 16, seed=42)
+    check(*run(c), c.expected())
+
+
+def test_rows_before_the_first_sequence_are_left():
+    c = Case([300, 40], [100, 40], 4, 2, 64, 16, seed=43)
+    o, total = c.expected(), c.total
+    c.qd = torch.cat([c.qd[:7], c.qd])
+    c.total += 7
+    out, lse = run(c, cu=i32([x + 7 for x in c.cu]))
+    assert torch.isnan(out[:7]).all() and torch.isnan(lse[:7]).all() and len(out) == total + 7
+    check(out[7:], lse[7:], o)

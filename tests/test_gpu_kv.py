@@ -5,6 +5,8 @@ import pytest
 import torch
 
 import kda_gated_delta_gate_b200 as kda
+import oracle
+from tests.attn_harness import check
 from tests.kv_model import KvModel
 
 pytestmark = pytest.mark.gpu
@@ -236,3 +238,61 @@ def test_append_bad_bounds_among_many_sequences(wrong):
         cu[i] = x
     order = [int(x) for x in np.random.default_rng(5).permutation(n)]
     _append_with_bounds(p, cu, order, total)
+
+
+def test_fork_and_truncate_of_many_slots():
+    """More pairs than one block has threads, refused ones among them, and pages that many slots share."""
+    n = 1300
+    p = Pair(pages=4000, page=16, heads=1, seqs=2 * n + 1, max_pages=3, layers=1)
+    p.call("reserve", list(range(n)), [(i * 11) % 49 for i in range(n)])
+    order = [int(x) for x in np.random.default_rng(8).permutation(n)]
+    p.call("fork", [x if x % 50 else -1 for x in order], [n + i for i in range(n)])
+    p.call("fork", [order[0]] * 4, [2 * n, 2 * n, 0, n])  # free, listed before, not empty, not empty or no pair's child
+    slots = list(range(2 * n))
+    lens = [int(x) for x in p.model.seq_len[:2 * n]]
+    p.call("truncate", slots[::-1], [x // 2 for x in lens[::-1]])
+    p.call("reserve", slots, [3] * (2 * n))  # copies of shared last pages, until the pages run out
+    p.call("compact")
+
+
+def test_a_captured_step_replayed():
+    """Reserve, append, attention, truncate, fork and compaction in one graph, replayed on changing inputs."""
+    page, H, D, seqs = 16, 2, 64, 5
+    p = Pair(pages=30, page=page, heads=1, dim=D, seqs=seqs, max_pages=6, layers=2, seed=4)
+    c, gen = p.cache, torch.Generator().manual_seed(9)
+    p.call("reserve", [0, 1, 2], [13, 30, 1])
+    slots, add, cu = _i32([2, 0, 1]), _i32([1, 1, 1]), _i32([0, 1, 2, 3])
+    parent, child, gone, none = _i32([1]), _i32([3]), _i32([3]), _i32([0])
+    k_new, v_new = (torch.zeros((3, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, out = (torch.zeros((3, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse, d = torch.zeros((3, H), device="cuda"), kda.dims(H, D, scale=0.125)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        kda.kda_kv_reserve(c, slots, add, 3)
+        for layer in range(2):
+            kda.kda_kv_append(c, layer, k_new, v_new, cu, slots, 3, 3)
+            kda.kda_attn_decode(c, layer, q, slots, 3, 1, out, d, lse=lse)
+        kda.kda_kv_truncate(c, gone, none, 1)
+        kda.kda_kv_fork(c, parent, child, 1)
+        kda.kda_kv_compact(c)
+    p.check()  # capture alone changes nothing
+    m = p.model
+    for step in range(25):
+        new = torch.randn((2, 3, D), generator=gen).bfloat16()
+        qs = torch.randn((3, H, D), generator=gen).bfloat16()
+        k_new.copy_(new[0]), v_new.copy_(new[1]), q.copy_(qs)
+        g.replay()
+        m.reserve([2, 0, 1], [1, 1, 1])
+        for layer in range(2):
+            m.append(layer, *[_bits(x).reshape(3, 1, D) for x in (k_new, v_new)], [0, 1, 2, 3], [2, 0, 1])
+        for i, s in enumerate([2, 0, 1]):
+            n = int(m.seq_len[s])
+            kv = [torch.from_numpy(np.stack([x[1, m.table[s, j // page], 0, j % page] for j in range(n)]).view(np.int16)).view(
+                torch.bfloat16).double().numpy() for x in (m.k, m.v)]
+            o, l, sp = zip(*[oracle.attention(qs[i, h:h + 1].double().numpy(), kv[0], kv[1], [n - 1], 0.125) for h in range(H)])
+            check(out[i:i + 1], lse[i:i + 1], (np.stack(o, 1), np.stack(l, 1), np.stack(sp, 1)))
+        m.truncate([3], [0])
+        m.fork([1], [3])
+        m.compact()
+        p.check()
