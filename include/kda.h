@@ -638,8 +638,8 @@ KDA_API int kda_graph_destroy(kda_graph *g);
 
 /* ---------------------------------------------------------------------------------
  * Paged key-value cache and its attention: the softmax-attention layers that a hybrid stack puts
- * between its KDA layers (Glm5NextLayer: a layer's mixer is the KDA block or attention over a
- * `PagedKvCache` with block tables). K and V rows live in fixed pages; a sequence is a slot of the
+ * between its KDA layers, with grouped heads of one head_dim for K and V. (Glm5NextLayer's own other
+ * mixer, over its `PagedKvCache` with block tables, is MLA/DSA, which this is not.) K and V rows live in fixed pages; a sequence is a slot of the
  * page table. One table serves every layer: a page index names that page of all layers' pools.
  *
  * Everything below is device memory of the caller; the struct itself is passed by host pointer.
@@ -757,7 +757,8 @@ KDA_API size_t kda_attn_decode_scratch_bytes(int N, int K, const kda_dims *dims,
  * too), a slot out of range or a length that is negative or past
  * max_pages pages is left unwritten, and so are the rows of a query tile that needs a table entry
  * that is no page; each latches KDA_ERR_INVALID_ARG. What pages hold past seq_len, or outside the
- * window of all rows of a query tile, has no effect; V rows that a row of the call sees must be finite. */
+ * window of all rows of a query tile, has no effect; V rows that a row of the call sees must be finite.
+ * B and heads <= 65535 (else KDA_ERR_UNSUPPORTED). */
 KDA_API int kda_attn_prefill(const kda_kv_cache *cache, int layer, const kda_bf16 *q, const int *cu_seqlens,
                              const int *slots, int B, int max_rows, int total_tokens, int window, int sinks,
                              kda_bf16 *out, float *lse, void *scratch, size_t scratch_bytes, const kda_dims *dims,

@@ -19,9 +19,12 @@
 // rounded p (one more product, with ones), so that the roundings cancel where few keys carry a row, and the one that
 // lse takes is that of the unrounded p.
 //
-// Measured (device time, HBM 6545 GB/s): 8 x 65500 tokens, 8 kv heads of 128, 4 rows per kv head: 316 us = 6.8 TB/s; 64
-// sequences of 125 to 8000 tokens, 16 rows: 188 us = 5.7 TB/s; one sequence of 4096: 11.9 us, nearly all of it the latency
-// of two launches and of the reads that depend on one another (slot, length, table, K, parts).
+// Measured (6545 GB/s is a copy's rate; reads alone go a little faster). 8 x 65500 tokens, 8 kv heads of 128, 4 rows per kv
+// head: 323 us = 6.6 TB/s in bursts of 20 on states in turn, 342 us = 6.3 TB/s in a loop, once the card is warm; 64 sequences of
+// 125 to 8000 tokens: 4 rows 171 us = 6.2 TB/s (181 in a loop), 16 rows 209 us = 5.1 TB/s in a loop; at head_dim 64, 4 rows, 92 us =
+// 5.8 TB/s. 256 sequences of 8000, window 1024, 4 sinks: 174 us = 6.2 TB/s, at head_dim 64 102 us = 5.3 TB/s. One sequence of 4096:
+// 11.9 us (one state, replayed, so out of L2), nearly all of it the latency of two launches and of the reads that depend on
+// one another (slot, length, table, K, parts).
 #include <algorithm>
 #include <type_traits>
 
@@ -30,8 +33,8 @@
 namespace kda {
 namespace {
 
-// Cached rows per tile: 32 KB of K and V at either head_dim (at 64, 64 ragged sequences: 104.6 us with 64 rows a tile and
-// four stages, 91.2 with 128 and two)
+// Cached rows per tile: 32 KB of K and V at either head_dim (at 64, 64 ragged sequences of 125 to 8000 tokens, 8 kv heads, 533 MB:
+// 104.6 us with 64 rows a tile and four stages, 91.2 with 128 and two)
 __host__ __device__ constexpr int tile_of(int D) { return D == 64 ? 128 : 64; }
 constexpr int kThreads = 128;  // four warps
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -148,8 +151,8 @@ __device__ __forceinline__ int run_of(long long tiles, int ctas, long long x) {
 //           at once goes to different banks.
 
 // Up to 8 rows: K q^T (keys x rows) and V^T p^T (channels x rows), rows on the products' short side, so that none is
-// spent on padding to 16. Thread: rows 2 (lane % 4) + e. Against the other form (8 x 65500 tokens, 4 rows per kv head):
-// 315 us against 320, and 316 against 340 once the card has warmed up, since it does half the products.
+// spent on padding to 16. Thread: rows 2 (lane % 4) + e. Against the other form (8 x 65500 tokens, 4 rows per kv head, replayed on
+// one state): 315 us against 320, and 316 against 340 after some seconds, since it does half the products.
 template <int D>
 struct RowsShort {
     static constexpr int KG = 4, ROWS = 8, KPW = tile_of(D) / KG;

@@ -27,17 +27,19 @@
 //
 // Rows of a cache tile that no row of the CTA sees (past the last token, before the window, pages that
 // left the table) are not loaded where they fill a page, and their V rows are zeroed in shared memory: what
-// they hold cannot reach a result. Every wait is bounded; one that gives up latches KDA_ERR_TIMEOUT.
+// they hold cannot reach a result. Every wait on a barrier is bounded; one that gives up latches KDA_ERR_TIMEOUT. Only tcgen05.alloc
+// waits as long as other CTAs of the SM hold its columns; each takes its columns once, so none waits for a second lot.
 //
-// Measured (BF16 1679 TFLOP/s in a burst, 1422 sustained): one prompt of 8192 tokens, 32 heads on 8 kv heads of 128, causal: 438 us =
-// 1255 TFLOP/s in a burst of 20, 500 us = 1099 once the power limit holds the clocks down; 4096 tokens 127 us, 2048 44;
-// head_dim 64: 387 us.
-// A tile takes about 2950 cycles for 256 rows at D = 128 (a row half's chain: softmax 1840, its two products 1220) and 3180 at
-// D = 64, where two softmax warps per scheduler keep the exponential unit 60 % busy. Before its first tile a CTA spends 6500 cycles
+// Measured (BF16 1679 TFLOP/s in a burst, 1422 sustained): one prompt of 8192 tokens, 32 heads on 8 kv heads of 128, causal: 452 us =
+// 1217 TFLOP/s in bursts of 20, 532 to 540 us = 1020 to 1034 in a loop, once the power limit holds the clocks down; 4096 tokens 132 us,
+// 2048 46; head_dim 64: 421 us, 440 in a loop. A chunk of 1024 rows behind 60000 tokens: 848 us (1197 TFLOP/s), at 64 835.
+// Without the second sum of weights a tile took about 2950 cycles for 256 rows at D = 128 (a row half's chain: softmax 1840, its two
+// products 1220) and 3180 at D = 64. There the exponential unit was 60 % busy and the issue slots 43 %: neither is full, two softmax
+// warps per scheduler do not cover each other's latencies. Before its first tile a CTA spends 6500 cycles
 // (bounds, slot, length and page entry, which depend on one another; Q; K) and after its last product 3000 on O; nothing runs
 // under these at D = 128. Tried and slower: the row's keys
 // split between two threads (549 us: the maxima's exchange), a quarter to a half of the exponentials as polynomials on
-// the FMA pipe (no gain at 128, 398 to 474 us against 386 at 64: issue, not the unit, is short), S read twice from TMEM instead of kept in
+// the FMA pipe (no gain at 128, 398 to 474 us against 386 at 64: the added instructions cost more than the unit's time saved), S read twice from TMEM instead of kept in
 // registers (506), both halves' key halves with an O of their own at D = 64 (424), Q requested before the set-up's barrier (463: spills;
 // later, with Q by whole rows and K of tile 0 too, 451 against 447), CTAs that take further tiles in place by cluster launch
 // control, the next tile's K and Q loaded under this one's end (438 against 434, 397 against 388 at 64: what it saves between tiles,

@@ -84,6 +84,7 @@ int attn_tiles(const kda_kv_cache *cache, int layer, const uint16_t *q, const in
 // Up to 32 query rows per kv head take the split form, more the tiled one. 64 sequences of 4000 tokens, 8 kv heads of 128,
 // 16 / 32 rows: 168 / 210 us split, 210 / 211 us tiled; 16 sequences of 500 to 8000 tokens, 32 rows: 75 split, 100 tiled (its
 // CTAs take whole walks where they are many). 48 and 64 rows: 297 and 306 us with the split form taken that far, 211 and 213 tiled.
+// (All tiled figures before its second sum of weights, which took 64 rows from 213 to 221.)
 inline bool few_rows(int rows, int heads, const kda_kv_cache *cache) {
     return static_cast<long long>(heads / cache->kv_heads) * rows <= 32;
 }
