@@ -210,14 +210,72 @@ def _call_on(scratch, name: str, *args) -> int:
 
 
 def scratch_buffer(nbytes: int, device, stream_handle: int):
-    """The cached scratch of (device, stream): a uint8 device tensor of at least nbytes."""
+    """The cached scratch of (device, stream): a uint8 device tensor of at least nbytes. While the stream is being captured a
+    buffer of the graph's own (_graph_scratch), so that graphs captured one after the other may run at once."""
     import torch
     dev = torch.device(device)
-    key = (dev.index if dev.index is not None else torch.cuda.current_device(), int(stream_handle))
+    dev = dev.index if dev.index is not None else torch.cuda.current_device()
+    if _is_captured(stream_handle):
+        return _graph_scratch(max(int(nbytes), 16), dev, stream_handle)
+    return _cached_scratch(nbytes, dev, stream_handle)
+
+
+def _cached_scratch(nbytes: int, dev: int, stream_handle: int):
+    key = (dev, int(stream_handle))
     buf = _SCRATCH.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = _SCRATCH[key] = _empty_on(max(int(nbytes), 16), key[0], key[1])
     return buf
+
+
+_GRAPHS = {}  # (device, stream, capture) -> None: the allocator has a pool for the graph; else the buffer kept for it
+_KEPT = []    # every such buffer
+
+
+def _graph_scratch(nbytes: int, dev: int, stream_handle: int):
+    """Scratch for the graph that the stream is being captured into. Under torch.cuda.graph it is memory of the graph's own
+    allocator pool, which stays with the graph. Where the stream is captured in another way (the CUDA API itself) it would go
+    back to the ordinary pool when the call returns, and later tensors would share it with the graph's replays: there one
+    buffer per capture is kept for good; callers that capture many such graphs pass `scratch`."""
+    key = (dev, stream_handle, _capture_id(stream_handle))
+    kept = _GRAPHS.get(key)
+    if kept is not None and kept.numel() >= nbytes:
+        return kept
+    buf = _empty_on(nbytes, dev, stream_handle)
+    if kept is not None or (key not in _GRAPHS and not _of_a_pool(buf)):
+        _GRAPHS[key] = buf
+        _KEPT.append(buf)
+    elif key not in _GRAPHS:
+        if len(_GRAPHS) >= 1024:
+            _GRAPHS.clear()
+        _GRAPHS[key] = None
+    return buf
+
+
+def _of_a_pool(t) -> bool:
+    """Whether tensor t lies in one of the allocator's pools for graphs (about 1 us a segment: asked once per capture)."""
+    import torch
+    try:
+        segments = torch.cuda.memory_snapshot()
+    except RuntimeError:  # another allocator, whose memory the graph holds itself
+        return True
+    at, dev = t.data_ptr(), t.device.index
+    return any(tuple(g["segment_pool_id"]) != (0, 0) for g in segments
+               if g["device"] == dev and g["address"] <= at < g["address"] + g["total_size"])
+
+
+def _capture_id(stream_handle: int) -> int:
+    """The number of the capture that the stream is in, 0 if it is in none."""
+    out = ctypes.c_ulonglong(0)
+    _call("kda_stream_capture_id", stream_handle, ctypes.byref(out))
+    return out.value
+
+
+def _is_captured(stream_handle: int) -> bool:
+    if _stream(None) == stream_handle:
+        import torch
+        return torch.cuda.is_current_stream_capturing()
+    return _capture_id(stream_handle) != 0
 
 
 def _empty_on(nbytes: int, dev: int, stream_handle: int):
@@ -733,64 +791,15 @@ def kda_attn_prefill_scratch_bytes(B: int, max_rows: int, total_tokens: int, d: 
 
 
 def _attn_scratch(fn, key, d: KdaDims, cache: KVCache, stream, stream_handle: int):
-    """The stream's cached buffer, of at least fn(*key) bytes; while the stream is being captured a buffer of the
-    graph's own (_graph_scratch), so that graphs captured one after the other may run at once."""
-    torch = cache._torch
+    """scratch_buffer of fn(*key) bytes, which are remembered."""
     need = cache._need.get((key, d.heads, d.head_dim))
     if need is None:
         if len(cache._need) >= 4096:  # sizes that change from call to call are not kept for good
             cache._need.clear()
         need = cache._need[key, d.heads, d.head_dim] = fn(*key, d, cache)
-    if stream is None or _stream(None) == stream_handle:
-        capturing = torch.cuda.is_current_stream_capturing()
-    else:
-        capturing = _capture_id(stream_handle) != 0
-    if capturing:
+    if cache._torch.cuda.is_current_stream_capturing() if stream is None else _is_captured(stream_handle):
         return _graph_scratch(max(need, 16), cache._device, stream_handle)
-    return scratch_buffer(need, cache._dev, stream_handle)
-
-
-_GRAPHS = {}  # (device, stream, capture) -> None: the allocator has a pool for the graph; else the buffer kept for it
-_KEPT = []    # every such buffer
-
-
-def _graph_scratch(nbytes: int, dev: int, stream_handle: int):
-    """Scratch for the graph that the stream is being captured into. Under torch.cuda.graph it is memory of the graph's own
-    allocator pool, which stays with the graph. Where the stream is captured in another way (the CUDA API itself) it would go
-    back to the ordinary pool when the call returns, and later tensors would share it with the graph's replays: there one
-    buffer per capture is kept for good; callers that capture many such graphs pass `scratch`."""
-    key = (dev, stream_handle, _capture_id(stream_handle))
-    kept = _GRAPHS.get(key)
-    if kept is not None and kept.numel() >= nbytes:
-        return kept
-    buf = _empty_on(nbytes, dev, stream_handle)
-    if kept is not None or (key not in _GRAPHS and not _of_a_pool(buf)):
-        _GRAPHS[key] = buf
-        _KEPT.append(buf)
-    elif key not in _GRAPHS:
-        if len(_GRAPHS) >= 1024:
-            _GRAPHS.clear()
-        _GRAPHS[key] = None
-    return buf
-
-
-def _of_a_pool(t) -> bool:
-    """Whether tensor t lies in one of the allocator's pools for graphs (about 1 us a segment: asked once per capture)."""
-    import torch
-    try:
-        segments = torch.cuda.memory_snapshot()
-    except RuntimeError:  # another allocator, whose memory the graph holds itself
-        return True
-    at, dev = t.data_ptr(), t.device.index
-    return any(tuple(g["segment_pool_id"]) != (0, 0) for g in segments
-               if g["device"] == dev and g["address"] <= at < g["address"] + g["total_size"])
-
-
-def _capture_id(stream_handle: int) -> int:
-    """The number of the capture that the stream is in, 0 if it is in none."""
-    out = ctypes.c_ulonglong(0)
-    _call("kda_stream_capture_id", stream_handle, ctypes.byref(out))
-    return out.value
+    return _cached_scratch(need, cache._device, stream_handle)
 
 
 def kda_attn_decode(cache: KVCache, layer: int, q, slots, N: int, K: int, out, d: KdaDims, window: int = 0,

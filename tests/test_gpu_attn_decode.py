@@ -365,3 +365,53 @@ def test_more_sequences_than_a_grid_dimension_has():
         k, v = torch.cat(rows)[:lens[i]].numpy(), torch.cat(vals)[:lens[i]].numpy()
         o, l, sp = zip(*[oracle.attention(q[i, h:h + 1].double().cpu().numpy(), k, v, [lens[i] - 1], 0.125) for h in range(heads)])
         check(out[i:i + 1], lse[i:i + 1], (np.stack(o, 1), np.stack(l, 1), np.stack(sp, 1)))
+
+
+def test_capture_numbers():
+    """A stream's capture is told apart from the next, and asking about another stream leaves it as it is."""
+    seen, x = set(), torch.zeros(4, device="cuda")
+    assert kda._capture_id(torch.cuda.current_stream().cuda_stream) == 0
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            seen.add(kda._capture_id(torch.cuda.current_stream().cuda_stream))
+            assert kda._capture_id(0) == 0  # the default stream
+            x.add_(1)
+        g.replay()
+    assert len(seen) == 2 and 0 not in seen
+    torch.cuda.synchronize()
+    assert (x == 2).all()
+
+
+def test_graphs_do_not_share_the_core_calls_scratch(monkeypatch):
+    """Graphs of the chunked prefill captured one after the other on torch's capture stream, and what that stream's calls take
+    afterwards: three buffers."""
+    d, at = kda.dims(2, 64), []
+    q, k, v = (torch.randn((64, 2, 64), device="cuda") for _ in range(3))
+    gate, beta, core = -torch.rand((64, 2, 64), device="cuda"), torch.rand((64, 2), device="cuda"), torch.empty((64, 2, 64), device="cuda")
+    state = torch.zeros((2, 64, 64), device="cuda")
+    ptrs, call, side = kda.ptr_array([state]), kda._call, torch.cuda.Stream()
+    f = lambda: kda.kda_chunk_prefill(q, k, v, gate, beta, ptrs, core, 1, 64, d)
+    f()
+    want, end = core.clone(), state.clone()
+
+    def noted(name, *args):
+        if name == "kda_chunk_prefill":
+            at.append(args[9])
+        return call(name, *args)
+
+    monkeypatch.setattr(kda, "_call", noted)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g, stream=side):
+            f()
+    with torch.cuda.stream(side):
+        f()
+    torch.cuda.synchronize()
+    assert len(set(at)) == 3
+    for g in graphs:
+        core.zero_(), state.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(core, want) and torch.equal(state, end)
